@@ -10,7 +10,7 @@ library.  The streams (x_sel, b; x, l^x, l^a) must be BF16, the library's
 input format: a tensor of another dtype is refused rather than converted."""
 import torch
 
-from . import scan
+from . import lm, scan
 
 
 def _need_bf16(**tensors):
@@ -149,3 +149,31 @@ def rglru_layer(x, w_x, b_x, w_a, b_a, alpha, reset=None, h0=None, *, K=16, G=0)
     """Input to output of the RG-LRU layer: gate projections, then the scan
     (one autograd node; x's gradient is rounded to BF16 once)."""
     return RglruLayer.apply(x, w_x, b_x, w_a, b_a, alpha, reset, h0, K, G)
+
+
+class BlockNorm(torch.autograd.Function):
+    """Residual sum and norms around a block: (x, y, gate, w_post, scale,
+    w_pre) -> (r, n), as lm.block_norm_fwd."""
+
+    @staticmethod
+    def forward(ctx, x, y, gate, w_post, scale, w_pre, eps, gate_act):
+        r, n, stats = lm.block_norm_fwd(x, y, gate, w_post, scale, w_pre, eps=eps, gate_act=gate_act)
+        ctx.save_for_backward(x, y, gate, w_post, scale, w_pre, stats)
+        ctx.eps, ctx.gate_act = eps, gate_act
+        ctx.set_materialize_grads(False)
+        return r, n
+
+    @staticmethod
+    def backward(ctx, dr, dn):
+        x, y, gate, w_post, scale, w_pre, stats = ctx.saved_tensors
+        # expanded cotangents (of a sum) have no rows to read: lay them out
+        dr = None if dr is None else dr.contiguous()
+        dn = None if dn is None else dn.contiguous()
+        g = lm.block_norm_bwd(x, y, gate, w_post, scale, w_pre, stats, dr, dn, eps=ctx.eps, gate_act=ctx.gate_act)
+        return (g["dx"], g["dy"], g.get("dgate"), g.get("dw_post"), g.get("dscale"), g["dw_pre"], None, None)
+
+
+def block_norm(x, y, gate, w_post, scale, w_pre, *, eps=1e-6, gate_act="none"):
+    """r = x + scale * act(gate) * norm(y) * w_post and n = norm(r) * w_pre
+    (without w_post and scale: r = x + act(gate) * y); returns (r, n)."""
+    return BlockNorm.apply(x, y, gate, w_post, scale, w_pre, eps, gate_act)

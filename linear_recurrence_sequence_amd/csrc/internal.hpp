@@ -43,6 +43,10 @@ enum KernelId {
     K_GATE_PROJ_ADJ,
     K_RGLRU_FWD_SCAN,
     K_RGLRU_BWD_SCAN,
+    K_LM_NORM,
+    K_LM_NORM_BWD,
+    K_LM_NORM_REDUCE,
+    K_LM_ADAMW,
     K_NUM_KERNELS
 };
 

@@ -1,0 +1,404 @@
+// lm_norm.hip -- the norms before and after a block, with its gate and
+// residual scale, forward and backward.
+//
+// For a row of width d, with y the block's output, g its gate logits and x
+// the residual stream (FP32 arithmetic; without w_post and scale the first
+// norm and both weights are left out):
+//   u = scale act(g) (y rs1) w_post,  r = x + u,  n = (r rs2) w_pre,
+//   rs1 = (mean y^2 + eps)^-1/2,  rs2 = (mean r^2 + eps)^-1/2.
+// Backward, from x, y, g and the kept (rs1, rs2) of each row:
+//   t = dn w_pre, rh = r rs2, v = dr + rs2 (t - rh mean(t rh)), dx = v,
+//   q = v scale act w_post, yh = y rs1, dy = rs1 (q - yh mean(q yh)),
+//   dgate = v scale yh w_post act',
+//   column sums: dw_pre = sum dn rh and S = sum v act yh, of which both
+//   dw_post = scale S and dscale = w_post S follow.
+//
+// Bound by memory: each row is read once into registers, both reductions and
+// every output come from there.  A row belongs to W waves of a workgroup, each
+// lane holding NV groups of 4 consecutive elements, 256 W elements apart, so
+// every load of a wave covers whole lines.  With W = 1 a workgroup holds four
+// rows and needs no barrier.  Workgroups walk over rows with the weights in
+// registers, and the backward keeps its column sums there until the end.
+#include "lm.hpp"
+
+namespace lrs {
+namespace {
+
+constexpr int MAX_WAVES = 16;
+
+// Sum over the row's waves.  `slot` alternates between calls, so one barrier
+// a reduction is enough: a slot is written again only after the barrier of the
+// reduction in between.
+template <bool ONE>
+__device__ __forceinline__ float row_sum(float v, float (*slots)[MAX_WAVES], int slot, int waves) {
+    v = wave_sum(v);
+    if (ONE) return v;
+    if ((threadIdx.x & 63) == 0) slots[slot][threadIdx.x >> 6] = v;
+    __syncthreads();
+    float s = 0.0f;
+    for (int i = 0; i < waves; ++i) s += slots[slot][i];
+    return s;
+}
+
+__device__ __forceinline__ float sigmoid(float g) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g));
+}
+
+// Which elements a lane holds: group c starts at column c * 4 T + 4 t.
+template <class T, bool TAIL>
+__device__ __forceinline__ Quad<T> row_load(const T* row, int col, int d) {
+    if (col + 4 <= d) return Quad<T>::load(row + col);
+    if (TAIL && col < d) return Quad<T>::load_some(row + col, d - col);
+    return Quad<T>::zero();
+}
+template <class T, bool TAIL>
+__device__ __forceinline__ void row_store(T* row, int col, int d, const float* f) {
+    if (col + 4 <= d) Quad<T>::store(row + col, f);
+    else if (TAIL && col < d) Quad<T>::store_some(row + col, f, d - col);
+}
+template <bool TAIL>
+__device__ __forceinline__ void weight_load(const float* w, int col, int d, float missing, float* f) {
+    if (w) {
+        row_load<float, TAIL>(w, col, d).get(f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = missing;
+    }
+}
+
+// TAIL: d is not a multiple of 4.  ONE: a row is one wave's.
+template <class ST, class BR, int NV, bool ONE, bool TAIL>
+__global__ __launch_bounds__(ONE ? 256 : 1024) void norm_fwd_kernel(const NormArgs a) {
+    __shared__ float slots[2][MAX_WAVES];
+    const int T = ONE ? 64 : blockDim.x, t = ONE ? threadIdx.x & 63 : threadIdx.x, waves = T >> 6;
+    const int per = ONE ? 4 : 1, mine = ONE ? threadIdx.x >> 6 : 0;
+    const bool full = a.w_post != nullptr, gated = a.gate != nullptr, silu = a.gate_act == 2;
+    const float inv_d = 1.0f / (float)a.d;
+    float w1[NV][4], w2[NV][4];
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int col = c * 4 * T + 4 * t;
+        float sc[4];
+        weight_load<TAIL>(a.w_post, col, a.d, 1.0f, w1[c]);
+        weight_load<TAIL>(a.scale, col, a.d, 1.0f, sc);
+        weight_load<TAIL>(a.w_pre, col, a.d, 1.0f, w2[c]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w1[c][i] *= sc[i];  // scale and w_post act as one factor of u
+    }
+    for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < a.rows; row0 += (int64_t)gridDim.x * per) {
+        const int64_t row = row0 + mine;
+        if (ONE && row >= a.rows) break;  // no barrier in this form
+        Quad<ST> qx[NV];
+        Quad<BR> qy[NV], qg[NV];
+        const ST* x = static_cast<const ST*>(a.x) + row * a.x_stride;
+        const BR* y = static_cast<const BR*>(a.y) + row * a.y_stride;
+        const BR* g = static_cast<const BR*>(a.gate) + row * a.gate_stride;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int col = c * 4 * T + 4 * t;
+            qy[c] = row_load<BR, TAIL>(y, col, a.d);
+            if (gated) qg[c] = row_load<BR, TAIL>(g, col, a.d);
+            qx[c] = row_load<ST, TAIL>(x, col, a.d);
+        }
+        float rs1 = 1.0f;
+        if (full) {
+            float s = 0.0f;
+#pragma unroll
+            for (int c = 0; c < NV; ++c) {
+                float f[4];
+                qy[c].get(f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s = fmaf(f[i], f[i], s);
+            }
+            rs1 = 1.0f / sqrtf(row_sum<ONE>(s, slots, 0, waves) * inv_d + a.eps);
+        }
+        float r[NV][4], s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            float f[4], u[4];
+            qy[c].get(u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = u[i] * rs1 * w1[c][i];
+            if (gated) {
+                qg[c].get(f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float sg = sigmoid(f[i]);
+                    u[i] *= silu ? sg * f[i] : sg;
+                }
+            }
+            qx[c].get(f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                r[c][i] = f[i] + u[i];
+                s = fmaf(r[c][i], r[c][i], s);
+            }
+        }
+        const float rs2 = 1.0f / sqrtf(row_sum<ONE>(s, slots, 1, waves) * inv_d + a.eps);
+        ST* ro = static_cast<ST*>(a.r) + row * a.d;
+        BR* no = static_cast<BR*>(a.n) + row * a.d;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int col = c * 4 * T + 4 * t;
+            row_store<ST, TAIL>(ro, col, a.d, r[c]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[c][i] = r[c][i] * rs2 * w2[c][i];
+            row_store<BR, TAIL>(no, col, a.d, r[c]);
+        }
+        if (t == 0) {
+            a.stats[2 * row] = rs1;
+            a.stats[2 * row + 1] = rs2;
+        }
+        // the plain form has one reduction a row: keep its slot from being written while others still read it
+        if (!ONE && !full) __syncthreads();
+    }
+}
+
+template <class ST, class BR, int NV, bool ONE, bool TAIL>
+__global__ __launch_bounds__(ONE ? 256 : 1024) void norm_bwd_kernel(const NormArgs a) {
+    __shared__ float slots[2][MAX_WAVES];
+    const int T = ONE ? 64 : blockDim.x, t = ONE ? threadIdx.x & 63 : threadIdx.x, waves = T >> 6;
+    const int per = ONE ? 4 : 1, mine = ONE ? threadIdx.x >> 6 : 0;
+    const bool full = a.w_post != nullptr, gated = a.gate != nullptr, silu = a.gate_act == 2;
+    const float inv_d = 1.0f / (float)a.d;
+    float w1[NV][4], w2[NV][4], sum2[NV][4], sums[NV][4];
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int col = c * 4 * T + 4 * t;
+        float sc[4];
+        weight_load<TAIL>(a.w_post, col, a.d, 1.0f, w1[c]);
+        weight_load<TAIL>(a.scale, col, a.d, 1.0f, sc);
+        weight_load<TAIL>(a.w_pre, col, a.d, 1.0f, w2[c]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w1[c][i] *= sc[i];
+            sum2[c][i] = sums[c][i] = 0.0f;
+        }
+    }
+    for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < a.rows; row0 += (int64_t)gridDim.x * per) {
+        const int64_t row = row0 + mine;
+        if (ONE && row >= a.rows) break;
+        Quad<ST> qx[NV], qr[NV];
+        Quad<BR> qy[NV], qg[NV], qn[NV];
+        const ST* x = static_cast<const ST*>(a.x) + row * a.x_stride;
+        const BR* y = static_cast<const BR*>(a.y) + row * a.y_stride;
+        const BR* g = static_cast<const BR*>(a.gate) + row * a.gate_stride;
+        const ST* dr = static_cast<const ST*>(a.dr) + row * a.dr_stride;
+        const BR* dn = static_cast<const BR*>(a.dn) + row * a.dn_stride;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int col = c * 4 * T + 4 * t;
+            qy[c] = row_load<BR, TAIL>(y, col, a.d);
+            if (gated) qg[c] = row_load<BR, TAIL>(g, col, a.d);
+            qx[c] = row_load<ST, TAIL>(x, col, a.d);
+            qn[c] = a.dn ? row_load<BR, TAIL>(dn, col, a.d) : Quad<BR>::zero();
+            qr[c] = a.dr ? row_load<ST, TAIL>(dr, col, a.d) : Quad<ST>::zero();
+        }
+        const float rs1 = a.stats[2 * row], rs2 = a.stats[2 * row + 1];
+        // rh = r rs2 and the first mean, of t rh; act(g) and yh are formed
+        // again where they are used, which costs less than keeping them
+        float rh[NV][4], s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            float u[4], f[4];
+            qy[c].get(u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = u[i] * rs1 * w1[c][i];
+            if (gated) {
+                qg[c].get(f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float sg = sigmoid(f[i]);
+                    u[i] *= silu ? sg * f[i] : sg;
+                }
+            }
+            qx[c].get(f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rh[c][i] = (f[i] + u[i]) * rs2;
+            qn[c].get(f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float p = f[i] * rh[c][i];
+                sum2[c][i] += p;
+                s = fmaf(p, w2[c][i], s);
+            }
+        }
+        const float m2 = row_sum<ONE>(s, slots, 0, waves) * inv_d;
+        // v, dx, dgate, the column sum S, and q yh for the second mean
+        ST* dx = static_cast<ST*>(a.dx) + row * a.d;
+        BR* dy = static_cast<BR*>(a.dy) + row * a.d;
+        BR* dg = static_cast<BR*>(a.dgate) + row * a.d;
+        s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int col = c * 4 * T + 4 * t;
+            float v[4], f[4], yh[4], da[4];
+            qr[c].get(v);
+            qn[c].get(f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += rs2 * (f[i] * w2[c][i] - rh[c][i] * m2);
+            row_store<ST, TAIL>(dx, col, a.d, v);
+            qy[c].get(yh);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) yh[i] *= rs1;
+            if (gated) {
+                qg[c].get(f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float sg = sigmoid(f[i]), slope = sg * (1.0f - sg);
+                    da[i] = v[i] * yh[i] * w1[c][i] * (silu ? sg + f[i] * slope : slope);
+                    v[i] *= silu ? sg * f[i] : sg;
+                }
+                row_store<BR, TAIL>(dg, col, a.d, da);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sums[c][i] += v[i] * yh[i];
+                rh[c][i] = v[i] * w1[c][i];  // q
+                s = fmaf(rh[c][i], yh[i], s);
+            }
+        }
+        const float m1 = full ? row_sum<ONE>(s, slots, 1, waves) * inv_d : 0.0f;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int col = c * 4 * T + 4 * t;
+            float yh[4];
+            qy[c].get(yh);
+            if (full) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) rh[c][i] = rs1 * (rh[c][i] - yh[i] * rs1 * m1);
+            }
+            row_store<BR, TAIL>(dy, col, a.d, rh[c]);
+        }
+        if (!ONE && !full) __syncthreads();
+    }
+    // column sums of this workgroup's rows (in a fixed order over its waves)
+    float* part = a.part + (int64_t)blockIdx.x * 2 * a.d;
+    if (ONE) {
+        __shared__ float buf[4][NV * 256];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (k) __syncthreads();
+#pragma unroll
+            for (int c = 0; c < NV; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) buf[mine][c * 256 + 4 * t + i] = k ? sums[c][i] : sum2[c][i];
+            __syncthreads();
+            for (int col = threadIdx.x; col < a.d; col += 256)
+                part[k * a.d + col] = (buf[0][col] + buf[1][col]) + (buf[2][col] + buf[3][col]);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < NV; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int col = c * 4 * T + 4 * t + i;
+                if (col < a.d) {
+                    part[col] = sum2[c][i];
+                    part[a.d + col] = sums[c][i];
+                }
+            }
+    }
+}
+
+// Column sums over the workgroups' partials, FP64 in a fixed order: 32
+// columns a workgroup, 32 lanes down each column.  blockIdx.y: dw_pre, or S
+// and from it dw_post and dscale.
+__global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* part, int blocks, int d, const float* w_post,
+                                                           const float* scale, float* dw_post, float* dscale,
+                                                           float* dw_pre) {
+    __shared__ double buf[32][33];
+    const int c = threadIdx.x & 31, lane = threadIdx.x >> 5, col = blockIdx.x * 32 + c, k = blockIdx.y;
+    double s = 0.0;
+    if (col < d)
+        for (int i = lane; i < blocks; i += 32) s += (double)part[((int64_t)i * 2 + k) * d + col];
+    buf[lane][c] = s;
+    __syncthreads();
+    for (int o = 16; o > 0; o >>= 1) {
+        if (lane < o) buf[lane][c] += buf[lane + o][c];
+        __syncthreads();
+    }
+    if (lane == 0 && col < d) {
+        const double v = buf[0][c];
+        if (k == 0) {
+            dw_pre[col] = (float)v;
+        } else {
+            dw_post[col] = (float)(v * (double)scale[col]);
+            dscale[col] = (float)(v * (double)w_post[col]);
+        }
+    }
+}
+
+// Waves of a row: NV groups of 256 columns a wave.  Few rows leave the chip
+// idle however they are spread, so they take one group a lane (the shortest
+// chain of loads and sums); many rows take two (four above 8192 columns, where
+// a row would not fit the 16 waves of a workgroup).
+struct Plan {
+    int nv, waves;
+};
+Plan plan(int64_t rows, int d) {
+    const int groups = (int)ceil_div(d, 256);
+    if (rows <= 512 && groups <= MAX_WAVES) return {1, groups};
+    if (groups <= 2 * MAX_WAVES) return {2, (int)ceil_div(groups, 2)};
+    return {4, (int)ceil_div(groups, 4)};
+}
+
+template <bool BWD, class ST, class BR, int NV, bool ONE>
+void launch_one(const NormArgs& a, dim3 g, dim3 b, hipStream_t s) {
+    if (a.d % 4 == 0) {
+        if (BWD) LRS_LAUNCH(K_LM_NORM_BWD, (norm_bwd_kernel<ST, BR, NV, ONE, false>), g, b, 0, s, a);
+        else LRS_LAUNCH(K_LM_NORM, (norm_fwd_kernel<ST, BR, NV, ONE, false>), g, b, 0, s, a);
+    } else {
+        if (BWD) LRS_LAUNCH(K_LM_NORM_BWD, (norm_bwd_kernel<ST, BR, NV, ONE, true>), g, b, 0, s, a);
+        else LRS_LAUNCH(K_LM_NORM, (norm_fwd_kernel<ST, BR, NV, ONE, true>), g, b, 0, s, a);
+    }
+}
+
+template <bool BWD, class ST, class BR>
+void launch_typed(const NormArgs& a, int blocks, hipStream_t s) {
+    const Plan p = plan(a.rows, a.d);
+    const dim3 g(blocks), b(p.waves == 1 ? 256 : 64 * p.waves);
+    if (p.waves == 1) {
+        if (p.nv == 1) launch_one<BWD, ST, BR, 1, true>(a, g, b, s);
+        else launch_one<BWD, ST, BR, 2, true>(a, g, b, s);
+    } else {
+        if (p.nv == 1) launch_one<BWD, ST, BR, 1, false>(a, g, b, s);
+        else if (p.nv == 2) launch_one<BWD, ST, BR, 2, false>(a, g, b, s);
+        else launch_one<BWD, ST, BR, 4, false>(a, g, b, s);
+    }
+}
+
+template <bool BWD>
+void launch_any(const NormArgs& a, int stream_f32, int branch_f32, int blocks, hipStream_t s) {
+    if (stream_f32) {
+        if (branch_f32) launch_typed<BWD, float, float>(a, blocks, s);
+        else launch_typed<BWD, float, uint16_t>(a, blocks, s);
+    } else {
+        if (branch_f32) launch_typed<BWD, uint16_t, float>(a, blocks, s);
+        else launch_typed<BWD, uint16_t, uint16_t>(a, blocks, s);
+    }
+}
+
+}  // namespace
+
+int lm_norm_bwd_blocks(int64_t rows, int d) {
+    const int per = plan(rows, d).waves == 1 ? 4 : 1;
+    return (int)std::min<int64_t>(ceil_div(rows, per), 1024);
+}
+
+hipError_t launch_norm_fwd(const NormArgs& a, int stream_f32, int branch_f32, hipStream_t s) {
+    const int per = plan(a.rows, a.d).waves == 1 ? 4 : 1;
+    launch_any<false>(a, stream_f32, branch_f32, (int)std::min<int64_t>(ceil_div(a.rows, per), 4096), s);
+    return hipGetLastError();
+}
+
+hipError_t launch_norm_bwd(const NormArgs& a, int stream_f32, int branch_f32, float* dw_post, float* dscale,
+                           float* dw_pre, hipStream_t s) {
+    const int blocks = a.rows ? lm_norm_bwd_blocks(a.rows, a.d) : 0;
+    if (blocks) launch_any<true>(a, stream_f32, branch_f32, blocks, s);
+    LRS_LAUNCH(K_LM_NORM_REDUCE, norm_reduce_kernel, dim3((unsigned)ceil_div(a.d, 32), a.w_post ? 2 : 1), dim3(1024), 0, s,
+               (const float*)a.part, blocks, a.d, a.w_post, a.scale, dw_post, dscale, dw_pre);
+    return hipGetLastError();
+}
+
+}  // namespace lrs
