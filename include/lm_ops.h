@@ -76,6 +76,42 @@ scan_status lm_block_norm_bwd(int64_t rows, int d, int stream_dtype, int branch_
                               void* workspace, size_t workspace_bytes, void* stream);
 
 /* ======================================================================
+ * Softmax cross entropy of a linear head, without the logits in memory.  For
+ * token t with hidden row h_t, vocabulary rows w_j and target y_t:
+ *   z_j = h_t . w_j   (softcap > 0: softcap tanh(h_t . w_j / softcap)),
+ *   lse_t = log sum_j exp z_j,  loss_t = lse_t - z_{y_t}.
+ * BF16 matrix-core products with FP32 sums.  A negative target: the token does
+ * not count (loss 0, and dloss is not read for it; lse is formed all the
+ * same).  A target >= v: loss and gradients are NaN.
+ *   h       bf16 [n, d], row stride h_stride (a multiple of 8)
+ *   w       bf16 [v, d]
+ *   target  int64 [n]
+ * 0 <= n, 1 <= v, both < 2^31 - 512; 8 <= d <= 65536, a multiple of 8; h and w
+ * 16-byte aligned.  A hidden row that does not count still enters
+ * dw as a zero times its values, so it has to be finite.
+ * ====================================================================== */
+
+/* Forward: loss, lse f32 [n].
+ *   workspace  lm_linear_ce_workspace_bytes(n, d, v, 0) bytes */
+size_t lm_linear_ce_workspace_bytes(int64_t n, int d, int64_t v, int backward);
+scan_status lm_linear_ce_fwd(int64_t n, int d, int64_t v, double softcap, const void* h, int64_t h_stride,
+                             const void* w, const int64_t* target, float* loss, float* lse,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward for the cotangents dloss f32 [n] and dlse f32 [n] (NULL = 0), from
+ * the forward's lse; the logits are formed again, some of the vocabulary at a
+ * time:
+ *   dz = (exp(z - lse) (dloss + dlse) - onehot(y) dloss) (1 - tanh^2),
+ *   dh = dz w,  dw = dz^T h,
+ * with dz rounded to BF16 for the two products.  dh [n, d] and dw [v, d] are of
+ * grad_dtype, dense.
+ *   workspace  lm_linear_ce_workspace_bytes(n, d, v, 1) bytes */
+scan_status lm_linear_ce_bwd(int64_t n, int d, int64_t v, double softcap, const void* h, int64_t h_stride,
+                             const void* w, const int64_t* target, const float* lse, const float* dloss,
+                             const float* dlse, void* dh, void* dw, int grad_dtype,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ======================================================================
  * AdamW over many tensors, in place.  For every element, in FP32:
  *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
  *   p = p (1 - lr decay) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps).

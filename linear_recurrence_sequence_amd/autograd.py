@@ -177,3 +177,31 @@ def block_norm(x, y, gate, w_post, scale, w_pre, *, eps=1e-6, gate_act="none"):
     """r = x + scale * act(gate) * norm(y) * w_post and n = norm(r) * w_pre
     (without w_post and scale: r = x + act(gate) * y); returns (r, n)."""
     return BlockNorm.apply(x, y, gate, w_post, scale, w_pre, eps, gate_act)
+
+
+class LinearCe(torch.autograd.Function):
+    """Softmax cross entropy of a linear head: (h, w, target) -> (loss, lse),
+    token by token, as lm.linear_ce_fwd."""
+
+    @staticmethod
+    def forward(ctx, h, w, target, softcap):
+        loss, lse = lm.linear_ce_fwd(h, w, target, softcap=softcap)
+        ctx.save_for_backward(h, w, target, lse)
+        ctx.softcap = softcap
+        ctx.set_materialize_grads(False)
+        return loss, lse
+
+    @staticmethod
+    def backward(ctx, dloss, dlse):
+        h, w, target, lse = ctx.saved_tensors
+        if dloss is None:
+            dloss = torch.zeros_like(lse)
+        g = lm.linear_ce_bwd(h, w, target, lse, dloss.float().contiguous(), None if dlse is None else dlse.float().contiguous(),
+                             softcap=ctx.softcap)
+        return g["dh"], g["dw"], None, None
+
+
+def linear_ce(h, w, target, *, softcap=0.0):
+    """Token-wise cross entropy of the logits h w^T (capped where softcap > 0),
+    which are not kept; returns (loss, lse).  Negative targets do not count."""
+    return LinearCe.apply(h, w, target, softcap)

@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libsamu_scan.so")
 ARCH = "gfx950"
 
 SOURCES = ["capi.cpp", "prefix.hip", "samu_fwd.hip", "samu_bwd.hip", "samu_decode.hip", "rglru.hip", "baseline.hip", "gate_proj.hip", "noalloc.hip",
-           "lm_capi.cpp", "lm_norm.hip", "lm_adamw.hip"]
+           "lm_capi.cpp", "lm_norm.hip", "lm_adamw.hip", "lm_ce.hip"]
 
 CXXFLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

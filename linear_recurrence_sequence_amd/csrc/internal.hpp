@@ -47,6 +47,11 @@ enum KernelId {
     K_LM_NORM_BWD,
     K_LM_NORM_REDUCE,
     K_LM_ADAMW,
+    K_LM_CE_STATS,
+    K_LM_CE_JOIN,
+    K_LM_CE_DZ,
+    K_LM_CE_DH,
+    K_LM_CE_DW,
     K_NUM_KERNELS
 };
 

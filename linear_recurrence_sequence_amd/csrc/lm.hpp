@@ -115,4 +115,32 @@ struct AdamwArgs {
 hipError_t launch_adamw(const AdamwArgs& a, uint32_t blocks, int param_f32, int grad_f32, bool master, bool bits8,
                         hipStream_t s);
 
+// -------------------------------------------------- linear cross entropy ---
+struct CeArgs {
+    int n, d, v;                // tokens, width, vocabulary
+    float cap;                  // 0: logits are not capped
+    const void* h;              // bf16 [n, d], row stride h_stride
+    int64_t h_stride;
+    const void* w;              // bf16 [v, d]
+    const int64_t* target;      // [n]; negative: the token does not count
+    // forward
+    float* part;                // [ce_parts(n, v), n] (maximum, sum of 2^(z - maximum)), base-2 logits
+    float* picked;              // [n] logit of the target
+    float *loss, *lse;          // [n]
+    // backward
+    const float *lse_in, *dloss, *dlse;
+    void* dz;                   // bf16 [n, chunk]
+    float* dh_part;             // [splits, n, d]
+    void *dh, *dw;
+    int grad_f32;
+};
+struct CePlan {
+    int chunk;   // vocabulary entries a backward pass takes at a time (a multiple of 256)
+    int splits;  // ranges of a chunk summed apart for dh
+};
+int ce_parts(int n, int v);
+CePlan ce_plan(int n, int d, int v);
+hipError_t launch_ce_fwd(const CeArgs& a, hipStream_t s);
+hipError_t launch_ce_bwd(const CeArgs& a, hipStream_t s);
+
 }  // namespace lrs

@@ -63,6 +63,8 @@ size_t span(int64_t rows, int64_t stride, int d, size_t size) {
 }
 
 constexpr int64_t kMaxRows = (int64_t)1 << 40;
+// a tile's 256 rows, or 64 steps, stay inside the 31-bit offsets of a buffer descriptor
+constexpr int64_t kMaxCeStride = (int64_t)1 << 21;
 
 scan_status norm_shape(const char* fn, int64_t rows, int d, int st, int br, int act, const void* gate,
                        const float* w_post, const float* scale, std::initializer_list<int64_t> strides) {
@@ -85,6 +87,41 @@ scan_status norm_shape(const char* fn, int64_t rows, int d, int st, int br, int 
 
 size_t norm_part_bytes(int64_t rows, int d) {
     return std::max<size_t>(256, (size_t)(rows > 0 ? lm_norm_bwd_blocks(rows, d) : 0) * 2 * d * sizeof(float));
+}
+
+// Buffers of the linear cross entropy inside the caller's workspace (base NULL: sizes only).
+size_t ce_layout(bool bwd, int n, int d, int v, void* base, CeArgs* a) {
+    char* p = static_cast<char*>(base);
+    size_t off = 0;
+    const auto take = [&](size_t bytes) {
+        void* at = p ? p + off : nullptr;
+        off += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    if (bwd) {
+        const CePlan pl = ce_plan(n, d, v);
+        a->dz = take((size_t)n * pl.chunk * 2);
+        a->dh_part = static_cast<float*>(take((size_t)pl.splits * n * d * 4));
+    } else {
+        a->part = static_cast<float*>(take((size_t)ce_parts(n, v) * n * 8));
+        a->picked = static_cast<float*>(take((size_t)n * 4));
+    }
+    return std::max<size_t>(off, 256);
+}
+
+bool ce_shape(int64_t n, int d, int64_t v) {
+    return n >= 0 && n < 0x7fffffff - 512 && v >= 1 && v < 0x7fffffff - 512 && d >= 8 && d <= 65536 && d % 8 == 0;
+}
+
+scan_status ce_check(const char* fn, int64_t n, int d, int64_t v, double cap, int64_t h_stride) {
+    if (!ce_shape(n, d, v))
+        return fail(SCAN_ERR_SHAPE, std::string(fn) + ": unsupported shape n=" + std::to_string(n) + " d=" + std::to_string(d) +
+                                        " v=" + std::to_string(v) + " (need v >= 1, 8 <= d <= 65536 a multiple of 8)");
+    if (!(cap >= 0.0) || !std::isfinite((float)cap) || (cap > 0.0 && (float)cap < 1e-30f))
+        return fail(SCAN_ERR_SHAPE, std::string(fn) + ": softcap must be 0 (none) or a positive number");
+    if (n > 0 && (h_stride % 8 != 0 || h_stride < 0 || h_stride > kMaxCeStride))
+        return fail(SCAN_ERR_SHAPE, std::string(fn) + ": the rows of h must lie a multiple of 8 elements apart");
+    return SCAN_OK;
 }
 
 }  // namespace
@@ -179,6 +216,63 @@ scan_status lm_block_norm_bwd(int64_t rows, int d, int stream_dtype, int branch_
     return device_status(launch_norm_bwd(a, stream_dtype == SCAN_F32, branch_dtype == SCAN_F32, dw_post, dscale,
                                          dw_pre, (hipStream_t)stream),
                          "block norm backward");
+}
+
+// ----------------------------------------------- linear cross entropy ---
+size_t lm_linear_ce_workspace_bytes(int64_t n, int d, int64_t v, int backward) {
+    if (!ce_shape(n, d, v)) return 0;
+    CeArgs a{};
+    return ce_layout(backward != 0, (int)n, d, (int)v, nullptr, &a);
+}
+
+scan_status lm_linear_ce_fwd(int64_t n, int d, int64_t v, double softcap, const void* h, int64_t h_stride, const void* w,
+                             const int64_t* target, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+    scan_status st = ce_check("lm_linear_ce_fwd", n, d, v, softcap, h_stride);
+    if (st != SCAN_OK) return st;
+    if (n == 0) return SCAN_OK;
+    CeArgs a{};
+    const size_t need = ce_layout(false, (int)n, d, (int)v, nullptr, &a), nb = (size_t)n * 4;
+    const Arg ah{h, span(n, h_stride, d, 2), 16, "h"}, aw{w, (size_t)v * d * 2, 16, "w"}, at{target, (size_t)n * 8, 8, "target"},
+        ol{loss, nb, 4, "loss"}, oe{lse, nb, 4, "lse"}, ws{workspace, need, 16, "workspace"};
+    st = check_args({ah, aw, at, ol, oe, ws}, {});
+    if (st != SCAN_OK) return st;
+    if (workspace_bytes < need)
+        return fail(SCAN_ERR_WORKSPACE, "lm_linear_ce_fwd: workspace_bytes " + std::to_string(workspace_bytes) + " < " +
+                                            std::to_string(need));
+    st = check_alias({ah, aw, at}, {ol, oe, ws});
+    if (st != SCAN_OK) return st;
+    ce_layout(false, (int)n, d, (int)v, workspace, &a);
+    a.n = (int)n, a.d = d, a.v = (int)v, a.cap = (float)softcap;
+    a.h = h, a.h_stride = h_stride, a.w = w, a.target = target;
+    a.loss = loss, a.lse = lse;
+    return device_status(launch_ce_fwd(a, (hipStream_t)stream), "linear cross entropy");
+}
+
+scan_status lm_linear_ce_bwd(int64_t n, int d, int64_t v, double softcap, const void* h, int64_t h_stride, const void* w,
+                             const int64_t* target, const float* lse, const float* dloss, const float* dlse, void* dh,
+                             void* dw, int grad_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    scan_status st = ce_check("lm_linear_ce_bwd", n, d, v, softcap, h_stride);
+    if (st != SCAN_OK) return st;
+    if (!dtype_ok(grad_dtype)) return fail(SCAN_ERR_SHAPE, "lm_linear_ce_bwd: grad_dtype must be SCAN_BF16 or SCAN_F32");
+    CeArgs a{};
+    const size_t need = ce_layout(true, (int)n, d, (int)v, nullptr, &a), nb = (size_t)n * 4, g = dtype_size(grad_dtype);
+    const Arg ah{h, span(n, h_stride, d, 2), 16, "h"}, aw{w, (size_t)v * d * 2, 16, "w"}, at{target, (size_t)n * 8, 8, "target"},
+        ae{lse, nb, 4, "lse"}, al{dloss, nb, 4, "dloss"}, az{dlse, nb, 4, "dlse"}, oh{dh, (size_t)n * d * g, 16, "dh"},
+        ow{dw, (size_t)v * d * g, 16, "dw"}, ws{workspace, need, 16, "workspace"};
+    st = n > 0 ? check_args({ah, aw, at, ae, al, oh, ow, ws}, {az}) : check_args({ow}, {});
+    if (st != SCAN_OK) return st;
+    if (workspace_bytes < need && n > 0)
+        return fail(SCAN_ERR_WORKSPACE, "lm_linear_ce_bwd: workspace_bytes " + std::to_string(workspace_bytes) + " < " +
+                                            std::to_string(need));
+    st = check_alias({ah, aw, at, ae, al, az}, {oh, ow, ws});
+    if (st != SCAN_OK) return st;
+    ce_layout(true, (int)n, d, (int)v, workspace, &a);
+    a.n = (int)n, a.d = d, a.v = (int)v, a.cap = (float)softcap;
+    a.h = h, a.h_stride = h_stride, a.w = w, a.target = target;
+    a.lse_in = lse, a.dloss = dloss, a.dlse = dlse;
+    a.dh = dh, a.dw = dw, a.grad_f32 = grad_dtype == SCAN_F32;
+    return device_status(launch_ce_bwd(a, (hipStream_t)stream), "linear cross entropy backward");
 }
 
 // --------------------------------------------------------------- AdamW ---

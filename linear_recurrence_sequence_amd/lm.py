@@ -35,6 +35,12 @@ def lib():
     L.lm_block_norm_bwd_workspace_bytes.restype = sz
     L.lm_block_norm_bwd.argtypes = [i64, i, i, i, i] + [vp, i64] * 3 + [vp] * 4 + [vp, i64] * 2 + [vp] * 6 + [vp, sz, vp]
     L.lm_block_norm_bwd.restype = i
+    L.lm_linear_ce_workspace_bytes.argtypes = [i64, i, i64, i]
+    L.lm_linear_ce_workspace_bytes.restype = sz
+    L.lm_linear_ce_fwd.argtypes = [i64, i, i64, dbl, vp, i64, vp, vp, vp, vp, vp, sz, vp]
+    L.lm_linear_ce_fwd.restype = i
+    L.lm_linear_ce_bwd.argtypes = [i64, i, i64, dbl, vp, i64] + [vp] * 7 + [i, vp, sz, vp]
+    L.lm_linear_ce_bwd.restype = i
     L.lm_adamw_step.argtypes = [i, i, i, i] + [vp] * 9 + [dbl] * 4 + [i64, vp]
     L.lm_adamw_step.restype = i
     _lib = L
@@ -174,6 +180,81 @@ def block_norm_bwd(x, y, gate, w_post, scale, w_pre, stats, dr, dn, *, eps=1e-6,
                                  _p(out["dw_pre"]), _p(workspace), _nbytes(workspace), _stream(stream))
     _check(st, "lm_block_norm_bwd")
     return out
+
+
+# ---------------------------------------------------- linear cross entropy ---
+def _ce_args(h, w, target):
+    _want(h, "h", _BF16)
+    _want(w, "w", _BF16)
+    if h.dim() < 1 or w.dim() != 2 or h.shape[-1] != w.shape[1]:
+        raise ValueError(f"h must be [..., d] and w [v, d], got shapes {tuple(h.shape)} and {tuple(w.shape)}")
+    _want(target, "target", torch.int64, h.shape[:-1])
+    _dense(w, "w")
+    _dense(target, "target")
+    _same_device(h, w=w, target=target)
+    return target.numel(), w.shape[1], w.shape[0], _row_stride(h, "h")
+
+
+def _ce_workspace(n, d, v, backward, workspace, dev):
+    need = lib().lm_linear_ce_workspace_bytes(n, d, v, backward)
+    if need == 0:
+        raise ValueError(f"unsupported shape: {n} tokens, width {d}, vocabulary {v} (the width must be a multiple of 8 in 8..65536)")
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    _want_bytes(workspace, "workspace", need)
+    return workspace
+
+
+def linear_ce_fwd(h, w, target, *, softcap=0.0, loss=None, lse=None, workspace=None, stream=None):
+    """Cross entropy of a linear head, token by token, without its logits:
+        z = h w^T (softcap > 0: softcap * tanh(z / softcap)),
+        lse = logsumexp(z),  loss = lse - z[target].
+
+    h [..., d] BF16 (rows may lie apart, 16-byte aligned), w [v, d] BF16, target
+    [...] int64; a negative target does not count (loss 0).  Returns (loss, lse)
+    FP32 [...]."""
+    n, d, v, sh = _ce_args(h, w, target)
+    dev = h.device
+    out = []
+    for t, name in ((loss, "loss"), (lse, "lse")):
+        if t is None:
+            t = torch.empty(target.shape, dtype=_F32, device=dev)
+        else:
+            _want(t, name, _F32, target.shape)
+            _dense(t, name)
+        out.append(t)
+    loss, lse = out
+    workspace = _ce_workspace(n, d, v, 0, workspace, dev)
+    st = lib().lm_linear_ce_fwd(n, d, v, softcap, _p(h), sh, _p(w), _p(target), _p(loss), _p(lse), _p(workspace),
+                                _nbytes(workspace), _stream(stream))
+    _check(st, "lm_linear_ce_fwd")
+    return loss, lse
+
+
+def linear_ce_bwd(h, w, target, lse, dloss, dlse=None, *, softcap=0.0, grad_dtype=_BF16, dh=None, dw=None,
+                  workspace=None, stream=None):
+    """Gradients of linear_ce_fwd for the cotangents dloss and dlse (FP32, as
+    the target; dlse None = 0), from its lse.  Returns dict(dh, dw) of
+    grad_dtype."""
+    n, d, v, sh = _ce_args(h, w, target)
+    dev = h.device
+    for t, name in ((lse, "lse"), (dloss, "dloss"), (dlse, "dlse")):
+        _want(t, name, _F32, target.shape, optional=name == "dlse")
+        _dense(t, name)
+    _code(grad_dtype)
+    if dh is None:
+        dh = torch.empty(h.shape, dtype=grad_dtype, device=dev)
+    if dw is None:
+        dw = torch.empty(w.shape, dtype=dh.dtype, device=dev)
+    for t, name, shape in ((dh, "dh", h.shape), (dw, "dw", w.shape)):
+        _want(t, name, _DTYPES if name == "dh" else dh.dtype, shape)
+        _dense(t, name)
+    _same_device(h, lse=lse, dloss=dloss, dlse=dlse, dh=dh, dw=dw)
+    workspace = _ce_workspace(n, d, v, 1, workspace, dev)
+    st = lib().lm_linear_ce_bwd(n, d, v, softcap, _p(h), sh, _p(w), _p(target), _p(lse), _p(dloss), _p(dlse), _p(dh),
+                                _p(dw), _code(dh.dtype), _p(workspace), _nbytes(workspace), _stream(stream))
+    _check(st, "lm_linear_ce_bwd")
+    return dict(dh=dh, dw=dw)
 
 
 # ------------------------------------------------------------------- AdamW ---

@@ -137,6 +137,66 @@ def test_norm_bwd_abi_rejects():
     assert L.lm_block_norm_bwd_workspace_bytes(0, 24) > 0
 
 
+# ---------------------------------------------------- linear cross entropy ---
+def ce_args(**over):
+    a = dict(h=torch.zeros(5, 24, dtype=bf), w=torch.zeros(40, 24, dtype=bf), target=torch.zeros(5, dtype=torch.int64))
+    a.update(over)
+    return list(a.values())
+
+
+@pytest.mark.parametrize("over,kw,msg", [
+    (dict(h=torch.zeros(5, 24)), {}, "h has dtype"),
+    (dict(w=torch.zeros(40, 24)), {}, "w has dtype"),
+    (dict(w=torch.zeros(40, 16, dtype=bf)), {}, "got shapes"),
+    (dict(w=torch.zeros(24, 40, dtype=bf).t()), {}, "w must be contiguous"),
+    (dict(h=torch.zeros(24, 5, dtype=bf).t()), {}, "h must have dense columns"),
+    (dict(target=torch.zeros(5, dtype=torch.int32)), {}, "target has dtype"),
+    (dict(target=torch.zeros(4, dtype=torch.int64)), {}, "target has shape"),
+    (dict(h=torch.zeros(5, 20, dtype=bf), w=torch.zeros(40, 20, dtype=bf)), {}, "unsupported shape"),
+    ({}, dict(loss=torch.zeros(5, dtype=bf)), "loss has dtype"),
+    ({}, dict(lse=torch.zeros(6)), "lse has shape"),
+    ({}, dict(workspace=torch.zeros(16, dtype=torch.uint8)), "workspace holds"),
+    ({}, {}, "device tensor"),
+])
+def test_ce_binding_rejects(over, kw, msg):
+    from linear_recurrence_sequence_amd import lm
+    with pytest.raises(ValueError, match=msg):
+        lm.linear_ce_fwd(*ce_args(**over), **kw)
+
+
+def test_ce_bwd_binding_rejects():
+    from linear_recurrence_sequence_amd import lm
+    ok = dict(lse=torch.zeros(5), dloss=torch.zeros(5), dlse=torch.zeros(5))
+    for over, msg in ((dict(lse=torch.zeros(4)), "lse has shape"), (dict(dloss=None), "dloss is required"),
+                      (dict(dlse=torch.zeros(5, dtype=bf)), "dlse has dtype"), (dict(dh=torch.zeros(5, 24), dw=torch.zeros(40, 24, dtype=bf)), "dw has dtype"),
+                      (dict(dw=torch.zeros(40, 23, dtype=bf)), "dw has shape"), (dict(grad_dtype=torch.float16), "output dtype"),
+                      ({}, "device tensor")):
+        kw = {**ok, **over}
+        with pytest.raises(ValueError, match=msg):
+            lm.linear_ce_bwd(*ce_args(), kw.pop("lse"), kw.pop("dloss"), kw.pop("dlse"), **kw)
+
+
+@fake_pointers
+def test_ce_abi_rejects():
+    from linear_recurrence_sequence_amd import lm
+    L = lm.lib()
+    fwd = dict(n=5, d=24, v=40, cap=0.0, h=P(1), hs=24, w=P(2), t=P(3), loss=P(4), lse=P(5), ws=P(6), wn=1 << 20)
+    for over, status in ((dict(n=-1), -2), (dict(d=20), -2), (dict(d=0), -2), (dict(d=65544), -2), (dict(v=0), -2), (dict(v=1 << 31), -2),
+                         (dict(cap=-1.0), -2), (dict(cap=float("nan")), -2), (dict(cap=float("inf")), -2), (dict(hs=28), -2), (dict(hs=-24), -2),
+                         (dict(hs=1 << 22), -2), (dict(h=None), -1), (dict(t=None), -1), (dict(h=ctypes.c_void_p((1 << 20) + 8)), -3),
+                         (dict(w=ctypes.c_void_p((2 << 20) + 2)), -3), (dict(wn=16), -4), (dict(loss=P(3)), -6), (dict(lse=P(4)), -6),
+                         (dict(n=0, h=None, t=None), 0)):
+        assert L.lm_linear_ce_fwd(*{**fwd, **over}.values(), None) == status, over
+    bwd = dict(n=5, d=24, v=40, cap=0.0, h=P(1), hs=24, w=P(2), t=P(3), lse=P(4), dl=P(5), dlse=P(6), dh=P(7), dw=P(8), gd=0, ws=P(9), wn=1 << 20)
+    for over, status in ((dict(gd=2), -2), (dict(lse=None), -1), (dict(dl=None), -1), (dict(dh=None), -1), (dict(dw=None), -1), (dict(wn=16), -4),
+                         (dict(dh=P(1)), -6), (dict(dw=P(2)), -6), (dict(ws=P(8)), -6), (dict(dw=ctypes.c_void_p((8 << 20) + 4)), -3),
+                         (dict(n=0, dw=None), -1)):
+        assert L.lm_linear_ce_bwd(*{**bwd, **over}.values(), None) == status, over
+    assert L.lm_linear_ce_workspace_bytes(5, 20, 40, 1) == 0
+    # pieces of the vocabulary: the backward's workspace does not grow with n v
+    assert L.lm_linear_ce_workspace_bytes(8192, 2048, 128000, 1) < 8192 * 128000 // 2
+
+
 # ------------------------------------------------------------------- AdamW ---
 def adamw(**over):
     from linear_recurrence_sequence_amd import lm
