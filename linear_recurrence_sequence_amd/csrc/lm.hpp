@@ -130,6 +130,7 @@ struct CeArgs {
     // backward
     const float *lse_in, *dloss, *dlse;
     void* dz;                   // bf16 [n, chunk]
+    float* scale;               // [1] what dz is divided by
     float* dh_part;             // [splits, n, d]
     void *dh, *dw;
     int grad_f32;

@@ -32,11 +32,11 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
 // Scale of one block and the codes of this lane's four values.
 template <bool ROOT>
 __device__ __forceinline__ uint32_t encode(const float* x, float* scale) {
+#pragma clang fp contract(off)
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-    const float amax = __uint_as_float(wave_umax(top));
-    const float s = amax / 448.0f;
+    const float s = __uint_as_float(wave_umax(top)) * (1.0f / 448.0f);
     *scale = s < 0x1p-96f ? 0x1p-96f : s;
     const float inv = 1.0f / *scale;
     float q[4];
@@ -60,6 +60,16 @@ __device__ __forceinline__ void decode(uint32_t w, float s, float* x) {
 // Four code bytes; the first n where fewer belong to the tensor.
 __device__ __forceinline__ uint32_t code_some(const uint8_t* p, int n) {
     return (n > 0 ? p[0] : 0u) | (n > 1 ? (uint32_t)p[1] << 8 : 0u) | (n > 2 ? (uint32_t)p[2] << 16 : 0u);
+}
+
+// The new moments, each operation rounded by itself and the root correctly
+// rounded: a code is chosen at the borders between two values, so that every
+// evaluation of the formulas in FP32 has to come to the same codes.
+__device__ __forceinline__ void moments(const AdamwArgs& a, float g, float* m, float* v, float* root) {
+#pragma clang fp contract(off)
+    *m = *m * a.b1 + g * a.c1;
+    *v = *v * a.b2 + (g * g) * a.c2;
+    *root = sqrtf(*v);
 }
 
 template <class PT, class GT, bool MASTER, bool BITS8, bool TAIL>
@@ -128,11 +138,8 @@ __device__ __forceinline__ void update(const AdamwArgs& a, int t, int64_t base, 
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            m[i] = m[i] * a.b1 + gg[i] * a.c1;
-            v[i] = v[i] * a.b2 + gg[i] * gg[i] * a.c2;
-            // hardware square root and reciprocal, one unit in the last place each
-            // (the root's argument is lifted out of the subnormals, which the unit does not take)
-            root[i] = v[i] < 0x1p-96f ? __builtin_amdgcn_sqrtf(v[i] * 0x1p64f) * 0x1p-32f : __builtin_amdgcn_sqrtf(v[i]);
+            moments(a, gg[i], &m[i], &v[i], &root[i]);
+            // the reciprocal is the hardware's, within one unit in the last place
             const float upd = m[i] * __builtin_amdgcn_rcpf(root[i] * a.root_scale + a.eps);
             pp[i] = pp[i] * keep - a.step_size * upd;
         }

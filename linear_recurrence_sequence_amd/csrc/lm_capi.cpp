@@ -100,6 +100,7 @@ size_t ce_layout(bool bwd, int n, int d, int v, void* base, CeArgs* a) {
     };
     if (bwd) {
         const CePlan pl = ce_plan(n, d, v);
+        a->scale = static_cast<float*>(take(4));
         a->dz = take((size_t)n * pl.chunk * 2);
         a->dh_part = static_cast<float*>(take((size_t)pl.splits * n * d * 4));
     } else {

@@ -124,7 +124,29 @@ __global__ __launch_bounds__(1024) void ce_join_kernel(const CeArgs a, int parts
 }
 
 // ------------------------------------------------------------ backward ---
-// dz of vocabulary entries [v0, v0 + count), BF16 [n, ld]; columns from count
+// The scale dz is held at: the largest |dloss| or |dloss + dlse| of a counting
+// token.  BF16 rounds dloss itself, and where all tokens weigh the same it
+// would round each target's entry the same way, an error that no sum averages
+// out; over the scale, those entries are 1 - p.  Both products give it back.
+__global__ __launch_bounds__(1024) void ce_scale_kernel(const CeArgs a) {
+    __shared__ float buf[16];
+    float top = 0.0f;
+    for (int i = threadIdx.x; i < a.n; i += 1024) {
+        const float dl = a.target[i] < 0 ? 0.0f : fabsf(a.dloss[i]);
+        const float c = a.dlse ? fmaxf(dl, fabsf((a.target[i] < 0 ? 0.0f : a.dloss[i]) + a.dlse[i])) : dl;
+        if (c < 0x1p100f) top = fmaxf(top, c);  // a weight that is not finite stays with its token
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < 16; ++i) top = fmaxf(top, buf[i]);
+        *a.scale = top < 0x1p-100f ? 1.0f : top;
+    }
+}
+
+// dz / scale of vocabulary entries [vfirst, vfirst + count), BF16 [n, ld]; columns from count
 // to the next multiple of 64 are zeros.
 template <class T>
 __global__ __launch_bounds__(T::THREADS) void ce_dz_kernel(const CeArgs a, int np, int nq, int vfirst, int count, int ld) {
@@ -138,7 +160,7 @@ __global__ __launch_bounds__(T::THREADS) void ce_dz_kernel(const CeArgs a, int n
     const int lane = threadIdx.x & 63;
     const int v0 = tp * BM + T::wave_p() + 4 * (lane >> 4), t0 = tq * BN + T::wave_q() + (lane & 15);
     const int padded = (count + 63) / 64 * 64;
-    const float inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
+    const float inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f, inv_scale = 1.0f / *a.scale;
 #pragma unroll
     for (int j = 0; j < T::FN; ++j) {
         const int tok = t0 + 16 * j;
@@ -146,7 +168,8 @@ __global__ __launch_bounds__(T::THREADS) void ce_dz_kernel(const CeArgs a, int n
         const int64_t y = a.target[tok];
         float dl = y < 0 ? 0.0f : a.dloss[tok];
         if (y >= a.v) dl = __builtin_nanf("");
-        const float c = dl + (a.dlse ? a.dlse[tok] : 0.0f), base = a.lse_in[tok] * LOG2E;
+        const float c = (dl + (a.dlse ? a.dlse[tok] : 0.0f)) * inv_scale, base = a.lse_in[tok] * LOG2E;
+        dl *= inv_scale;
         const int64_t at = y - vfirst;
 #pragma unroll
         for (int i = 0; i < T::FM; ++i) {
@@ -209,6 +232,7 @@ __global__ __launch_bounds__(256) void ce_dh_join_kernel(const CeArgs a, int spl
     if (i >= total) return;
     f32acc_t s = reinterpret_cast<const f32acc_t*>(a.dh_part)[i];
     for (int k = 1; k < splits; ++k) s += reinterpret_cast<const f32acc_t*>(a.dh_part)[i + k * total];
+    s *= *a.scale;
     if (a.grad_f32) reinterpret_cast<f32acc_t*>(a.dh)[i] = s;
     else reinterpret_cast<u32x2_t*>(a.dh)[i] = u32x2_t{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
 }
@@ -222,6 +246,7 @@ __global__ __launch_bounds__(T::THREADS) void ce_dw_kernel(const CeArgs a, int n
     tile_of(np, nq, &tp, &tq);
     constexpr int BM = T::P_BYTES / 128, BN = T::Q_BYTES / 128;
     const int padded = (count + 63) / 64 * 64;
+    const float scale = *a.scale;
     T t;
     t.run(lds, Operand{a.h, a.h_stride, a.d}, Operand{a.dz, ld, padded}, tp * BM, tq * BN, 0, a.n);
     const int lane = threadIdx.x & 63;
@@ -235,7 +260,7 @@ __global__ __launch_bounds__(T::THREADS) void ce_dw_kernel(const CeArgs a, int n
             const int c = c0 + 16 * i;
             if (c >= a.d) continue;
             const int64_t at = (int64_t)(vfirst + v) * a.d + c;
-            const f32acc_t s = t.acc[i][j];
+            const f32acc_t s = t.acc[i][j] * scale;
             if (a.grad_f32) *reinterpret_cast<f32acc_t*>(static_cast<float*>(a.dw) + at) = s;
             else *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.dw) + at) = u32x2_t{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
         }
@@ -302,6 +327,7 @@ hipError_t launch_ce_bwd(const CeArgs& a, hipStream_t s) {
         return hipGetLastError();
     }
     const CePlan pl = ce_plan(a.n, a.d, a.v);
+    LRS_LAUNCH(K_LM_CE_JOIN, ce_scale_kernel, dim3(1), dim3(1024), 0, s, a);
     int used = 1;  // ranges of the first chunk, which is the longest
     for (int v0 = 0; v0 < a.v; v0 += pl.chunk) {
         const int count = std::min(pl.chunk, a.v - v0), ld = pl.chunk;
