@@ -49,6 +49,7 @@ enum KernelId {
     K_LM_ADAMW,
     K_LM_CE_STATS,
     K_LM_CE_JOIN,
+    K_LM_CE_LIST,
     K_LM_CE_DZ,
     K_LM_CE_DH,
     K_LM_CE_DW,

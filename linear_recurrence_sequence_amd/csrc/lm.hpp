@@ -116,6 +116,10 @@ hipError_t launch_adamw(const AdamwArgs& a, uint32_t blocks, int param_f32, int 
                         hipStream_t s);
 
 // -------------------------------------------------- linear cross entropy ---
+struct CeToken {    // a token as the backward takes it
+    float c, base, dl;  // (dloss + dlse) / scale, lse in base 2, dloss / scale
+    int target;         // -1: none
+};
 struct CeArgs {
     int n, d, v;                // tokens, width, vocabulary
     float cap;                  // 0: logits are not capped
@@ -124,22 +128,27 @@ struct CeArgs {
     const void* w;              // bf16 [v, d]
     const int64_t* target;      // [n]; negative: the token does not count
     // forward
-    float* part;                // [ce_parts(n, v), n] (maximum, sum of 2^(z - maximum)), base-2 logits
+    float* part;                // [ce_parts(n, d, v), n] (maximum, sum of 2^(z - maximum)), base-2 logits
     float* picked;              // [n] logit of the target
     float *loss, *lse;          // [n]
     // backward
     const float *lse_in, *dloss, *dlse;
-    void* dz;                   // bf16 [n, chunk]
     float* scale;               // [1] what dz is divided by
-    float* dh_part;             // [splits, n, d]
+    int* active;                // [1] tokens that take part
+    int *list, *place;          // [n] their numbers; place in the list, -1 of the others
+    CeToken* token;             // [active]
+    void* packed;               // bf16 [active, d] their rows of h
+    void* dz;                   // bf16 [active, chunk]
+    float* dh_part;             // [splits, n, d], rows as listed
     void *dh, *dw;
     int grad_f32;
 };
 struct CePlan {
     int chunk;   // vocabulary entries a backward pass takes at a time (a multiple of 256)
     int splits;  // ranges of a chunk summed apart for dh
+    int dz, dh, dw;  // tile shapes of the three products
 };
-int ce_parts(int n, int v);
+int ce_parts(int n, int d, int v);
 CePlan ce_plan(int n, int d, int v);
 hipError_t launch_ce_fwd(const CeArgs& a, hipStream_t s);
 hipError_t launch_ce_bwd(const CeArgs& a, hipStream_t s);

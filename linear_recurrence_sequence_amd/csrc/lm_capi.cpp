@@ -101,10 +101,15 @@ size_t ce_layout(bool bwd, int n, int d, int v, void* base, CeArgs* a) {
     if (bwd) {
         const CePlan pl = ce_plan(n, d, v);
         a->scale = static_cast<float*>(take(4));
+        a->active = static_cast<int*>(take(4));
+        a->list = static_cast<int*>(take((size_t)n * 4));
+        a->place = static_cast<int*>(take((size_t)n * 4));
+        a->token = static_cast<CeToken*>(take((size_t)n * sizeof(CeToken)));
+        a->packed = take((size_t)n * d * 2);
         a->dz = take((size_t)n * pl.chunk * 2);
         a->dh_part = static_cast<float*>(take((size_t)pl.splits * n * d * 4));
     } else {
-        a->part = static_cast<float*>(take((size_t)ce_parts(n, v) * n * 8));
+        a->part = static_cast<float*>(take((size_t)ce_parts(n, d, v) * n * 8));
         a->picked = static_cast<float*>(take((size_t)n * 4));
     }
     return std::max<size_t>(off, 256);

@@ -37,7 +37,250 @@ constexpr int GEMM_BK = 64;
 // BM x BN tile, WM x WN waves; PT / QT: the operand lies as [k][rows].
 template <int BM, int BN, int WM, int WN, bool PT, bool QT>
 struct TileProduct {
-    static constexpr int WAVES = WM * WN, THREADS = WAVES * 64;
+    static constexpr int WAVES = WM * WN, THREADS = WAVES * 64, TILE_P = BM, TILE_Q = BN, WAVES_P = WM;
+    static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;          // fragments of a wave
+    static constexpr int HP = BM / 2, HQ = BN / 2, HM = FM / 2, HN = FN / 2;  // and of a half: rows, fragments of a wave
+    static constexpr bool ROOMY = WAVES == 4;  // one wave a SIMD: 512 registers
+    static constexpr int STAGE = (BM + BN) * GEMM_BK * 2, LDS_BYTES = 2 * STAGE;
+    f32acc_t acc[FM][FN];
+
+    // Bank spread of reduction step k in a transposed half of R rows, in units
+    // of 32 bytes: the 16 steps that a fragment read touches at once (4 of each 8
+    // of 32) lie on all eight 32-byte groups of the 64 banks, twice each.
+    template <int R>
+    static __device__ __forceinline__ int spread(int k) {
+        static_assert(R == 128 || R == 64, "256 or 128 bytes a step");
+        return R == 128 ? (k & 3) | ((k >> 3) & 1) << 2 : ((k >> 1) & 1) | ((k >> 3) & 1) << 1;
+    }
+
+    // Loads of an operand's tile, half by half: R rows a half, this wave's share of R / 8 loads of 1 KiB.
+    template <int R, bool TR>
+    struct Loader {
+        static constexpr int N = R / 8 / WAVES;
+        static_assert(R / 8 % WAVES == 0, "loads divide over the waves");
+        uint32_t off[2][N];  // byte offset of this lane's 16 bytes from the step's base
+        int piece;           // first reduction index of those 16 bytes within a step (where it is dense)
+        uint64_t base;
+        int64_t step;
+        uint32_t line;       // bytes from one reduction index to the next (where it is not dense)
+        int left;            // reduction indices from this step on
+        uint32_t to;         // LDS address of this wave's first load
+        __device__ __forceinline__ void init(const char* lds, const Operand& o, int row0, int k0, int k1) {
+            const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+            const char* b = static_cast<const char*>(o.p);
+            base = (uint64_t)(TR ? b + ((int64_t)k0 * o.ld + row0) * 2 : b + ((int64_t)row0 * o.ld + k0) * 2);
+            step = TR ? GEMM_BK * o.ld * 2 : GEMM_BK * 2;
+            line = (uint32_t)(o.ld * 2);
+            left = k1 - k0;
+            piece = ((lane % 8) ^ (lane / 8)) * 8;
+            to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)lds + wave * 1024;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const int L = wave + WAVES * j;
+                    if (TR) {
+                        constexpr int PIECES = R / 8, KROWS = 64 / PIECES;  // 16-byte pieces of a step, steps of one load
+                        const int k = L * KROWS + lane / PIECES;
+                        const int col = h * R + ((lane % PIECES) ^ (spread<R>(k) * 2)) * 8;
+                        off[h][j] = row0 + col < o.rows ? (uint32_t)((k * o.ld + col) * 2) : 0x80000000u;
+                    } else {
+                        const int r = h * R + 8 * L + lane / 8;
+                        off[h][j] = row0 + r < o.rows ? (uint32_t)((r * o.ld + piece) * 2) : 0x80000000u;
+                    }
+                }
+        }
+        // Requests load j of half h of the step, 64 x 16 bytes into LDS at `at`
+        // from this wave's place; beyond the last reduction index it writes zeros
+        // (past the descriptor's end, or, where the index is dense, lane by lane).
+        // In assembly, so that the compiler does not wait for it before the
+        // LDS reads of the other halves; it writes no register, and the
+        // wait stands before the barrier that hands the half over.
+        __device__ __forceinline__ void request(int at, int h, int j) {
+            const int some = left < 0 ? 0 : left < GEMM_BK ? left : GEMM_BK;
+            const uint32_t end = TR ? (uint32_t)__builtin_amdgcn_readfirstlane((int)(some * line)) : 0x7fffffffu;
+            const u32x4_t rsrc = {(uint32_t)base, (uint32_t)(base >> 32), end, 0x00020000u};
+            const uint32_t o = TR || piece < some ? off[h][j] : 0x80000000u;
+            asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds"
+                         :
+                         : "s"(to), "s"(at + WAVES * 1024 * j), "v"(o), "s"(rsrc)
+                         : "memory", "scc");
+        }
+        __device__ __forceinline__ void request_half(int at, int h) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) request(at, h, j);
+        }
+        __device__ __forceinline__ void advance() {
+            base += step;
+            left -= GEMM_BK;
+        }
+    };
+
+    // Fragment f (16 rows) of this wave's rows in a half, steps 32 kk to 32 kk + 31.
+    template <int R, bool TR>
+    struct Reader {
+        uint32_t at[TR ? 1 : 2];  // LDS addresses
+        __device__ __forceinline__ void init(const char* tile, int row) {
+            const int lane = threadIdx.x & 63;
+            const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)tile;
+            if constexpr (TR) {
+                // lane s of 16 reads 4 columns of one of 4 steps and receives its own column of all four
+                const int g = lane >> 4, s = lane & 15, k = 8 * g + (s >> 2);
+                at[0] = lds + k * (R * 2) + (((row / 16) ^ spread<R>(k)) * 32) + (s & 3) * 8;
+            } else {
+                const int r = row + (lane & 15);
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+                    at[kk] = lds + r * 128 + (((lane >> 4) + 4 * kk) ^ (r & 7)) * 16;
+            }
+        }
+        __device__ __forceinline__ bf16x8_t read(int f, int kk, int from) const {
+            typedef __attribute__((address_space(3))) s16x4_t lds4;
+            typedef __attribute__((address_space(3))) bf16x8_t lds8;
+            // With two waves a SIMD the address is formed where it is used: kept over the
+            // loop, those of all fragments and stages would not fit the registers.
+            uint32_t o = at[TR ? 0 : kk];
+            if (!ROOMY) asm volatile("" : "+v"(o));
+            if constexpr (TR) {  // f is below the power of two that divides the wave's first fragment: an XOR adds it
+                o = (o ^ (uint32_t)(f * 32)) + (uint32_t)(kk * 32 * (R * 2) + from);
+                s16x4_t v[2];
+                v[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)o);
+                v[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(o + 4 * (R * 2)));
+                return __builtin_bit_cast(bf16x8_t, v);
+            } else {
+                return *(const lds8*)(o + (uint32_t)(f * 16 * 128 + from));
+            }
+        }
+    };
+
+    // Row of the tile that fragment i of P (j of Q) of this wave starts at.
+    static __device__ __forceinline__ int row_p(int i) {
+        return i / HM * HP + (int)(threadIdx.x >> 6) / WN * (HM * 16) + i % HM * 16;
+    }
+    static __device__ __forceinline__ int row_q(int j) {
+        return j / HN * HQ + (int)(threadIdx.x >> 6) % WN * (HN * 16) + j % HN * 16;
+    }
+
+    // Byte offsets within a stage of half h of P and of Q.
+    static constexpr int at_p(int h) { return h * HP * GEMM_BK * 2; }
+    static constexpr int at_q(int h) { return BM * GEMM_BK * 2 + h * HQ * GEMM_BK * 2; }
+
+    struct State {
+        Loader<HP, PT> lp;
+        Loader<HQ, QT> lq;
+        Reader<HP, PT> rp;
+        Reader<HQ, QT> rq;
+        bf16x8_t a[2][HM][2], b[2][HN][2];  // fragments of each half: [half][fragment][kk]
+    };
+    static constexpr int LOADS = Loader<HP, PT>::N;
+    static_assert(LOADS == Loader<HQ, QT>::N, "a half of either operand is as many loads");
+
+    // One of four phases of a step: the products of half X of P and Y of Q.
+    // Between them stand the reads of the half that comes next (half RH of P
+    // or Q, at `from`) and loads of the step after the next (half LH, to `to`), so that neither
+    // the matrix cores nor the queues of LDS and memory wait for each other.
+    template <int X, int Y, bool READ_P, int RH, bool LOAD_P, int LH>
+    __device__ __forceinline__ void phase(State& s, int from, int to) {
+        constexpr int M = HM * HN * 2, READS = 2 * (READ_P ? HM : HN);
+#pragma unroll
+        for (int t = 0; t < M; ++t) {
+#pragma unroll
+            for (int r = 0; r < READS; ++r)
+                if (r * (M / 2) / READS == t) {
+                    if (READ_P) s.a[RH][r / 2][r % 2] = s.rp.read(r / 2, r % 2, from + at_p(RH));
+                    else s.b[RH][r / 2][r % 2] = s.rq.read(r / 2, r % 2, from + at_q(RH));
+                }
+#pragma unroll
+            for (int l = 0; l < LOADS; ++l)
+                if (l * M / LOADS + 1 == t) {
+                    if (LOAD_P) s.lp.request(to + at_p(LH), LH, l);
+                    else s.lq.request(to + at_q(LH), LH, l);
+                }
+            __builtin_amdgcn_sched_barrier(0);
+            const int kk = t / (HM * HN), i = t / HN % HM, j = t % HN;
+            f32acc_t& c = acc[X * HM + i][Y * HN + j];
+            if (ROOMY) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(s.a[X][i][kk]), "v"(s.b[Y][j][kk]));
+            else c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(s.a[X][i][kk], s.b[Y][j][kk], c, 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    // What the two phases before read is in registers, so that its place can be
+    // loaded again, and what the next two read (requested three pairs of phases
+    // ago) has landed.
+    static __device__ __forceinline__ void hand_over() {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(4 * LOADS) : "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    }
+
+    // Step whose first half of Q is F; its buffers are those of `stage`.
+    template <int F>
+    __device__ __forceinline__ void step(State& s) {
+        constexpr int stage = F * STAGE;
+        phase<0, F, false, 1 - F, true, 0>(s, stage, stage);
+        phase<0, 1 - F, true, 1, false, F>(s, stage, stage);
+        hand_over();
+        phase<1, 1 - F, true, 0, false, 1 - F>(s, STAGE - stage, stage);
+        s.lq.advance();
+        phase<1, F, false, 1 - F, true, 1>(s, STAGE - stage, stage);
+        s.lp.advance();
+        hand_over();
+    }
+
+    __device__ __forceinline__ void run(char* lds, const Operand& p, const Operand& q, int p0, int q0, int k0, int k1) {
+        State s;
+        s.lp.init(lds, p, p0, k0, k1);
+        s.lq.init(lds, q, q0, k0, k1);
+        s.rp.init(lds, row_p(0));
+        s.rq.init(lds, row_q(0));
+        // steps 0 and 1 in the order in which they are read
+        s.lp.request_half(at_p(0), 0);
+        s.lq.request_half(at_q(0), 0);
+        s.lq.request_half(at_q(1), 1);
+        s.lp.request_half(at_p(1), 1);
+        s.lp.advance();
+        s.lq.advance();
+        s.lp.request_half(STAGE + at_p(0), 0);
+        s.lq.request_half(STAGE + at_q(1), 1);
+        s.lq.request_half(STAGE + at_q(0), 0);
+        s.lp.request_half(STAGE + at_p(1), 1);
+        s.lp.advance();
+        s.lq.advance();
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = f32acc_t{0.f, 0.f, 0.f, 0.f};
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(6 * LOADS) : "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+            for (int j = 0; j < HN; ++j) s.b[0][j][kk] = s.rq.read(j, kk, at_q(0));
+#pragma unroll
+            for (int i = 0; i < HM; ++i) s.a[0][i][kk] = s.rp.read(i, kk, at_p(0));
+        }
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(4 * LOADS) : "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        // two steps at a time; where their number is odd the last is one of zeros
+        for (int k = k0; k < k1; k += 2 * GEMM_BK) {
+            step<0>(s);
+            step<1>(s);
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if (ROOMY) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+    }
+};
+
+// The same product for tiles of few rows, where a wave has too few fragments to
+// halve: the next step's tile is loaded while one step is multiplied.
+template <int BM, int BN, int WM, int WN, bool PT, bool QT>
+struct ThinProduct {
+    static constexpr int WAVES = WM * WN, THREADS = WAVES * 64, TILE_P = BM, TILE_Q = BN, WAVES_P = WM;
     static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
     static constexpr int P_BYTES = BM * GEMM_BK * 2, Q_BYTES = BN * GEMM_BK * 2, STAGE = P_BYTES + Q_BYTES;
     static constexpr int LDS_BYTES = 2 * STAGE;
@@ -140,6 +383,8 @@ struct TileProduct {
     // First row of P and of Q that this wave's fragments start at.
     static __device__ __forceinline__ int wave_p() { return (int)(threadIdx.x >> 6) / WN * (BM / WM); }
     static __device__ __forceinline__ int wave_q() { return (int)(threadIdx.x >> 6) % WN * (BN / WN); }
+    static __device__ __forceinline__ int row_p(int i) { return wave_p() + 16 * i; }
+    static __device__ __forceinline__ int row_q(int j) { return wave_q() + 16 * j; }
 
     __device__ __forceinline__ void run(char* lds, const Operand& p, const Operand& q, int p0, int q0, int k0, int k1) {
         Loader<BM, PT> lp;
