@@ -87,8 +87,9 @@ scan_status lm_block_norm_bwd(int64_t rows, int d, int stream_dtype, int branch_
  *   w       bf16 [v, d]
  *   target  int64 [n]
  * 0 <= n, 1 <= v, both < 2^31 - 512; 8 <= d <= 65536, a multiple of 8; h and w
- * 16-byte aligned.  A hidden row that does not count still enters
- * dw as a zero times its values, so it has to be finite.
+ * 16-byte aligned.  The backward works on the tokens with a weight alone
+ * (dloss of a token that counts, or dlse, not zero): the others cost it nothing, and
+ * whatever their hidden rows hold, NaN and infinities too, stays out of dw.
  * ====================================================================== */
 
 /* Forward: loss, lse f32 [n].

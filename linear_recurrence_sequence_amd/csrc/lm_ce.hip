@@ -6,7 +6,8 @@
 //   lse_t = log sum_j exp z_j,  loss_t = lse_t - z_{y_t} (0 where y_t < 0).
 // The forward product's tiles end in a running maximum and sum of each token
 // over the tile's vocabulary entries; a second small launch joins them.
-// Backward, vocabulary chunk by chunk: the logits are formed again, and
+// Backward, for the tokens that have a weight, vocabulary chunk by chunk: the
+// logits are formed again, and
 //   dz_j = (exp(z_j - lse_t) (dloss_t + dlse_t) - [j = y_t] dloss_t) (1 - tanh^2)
 // is rounded to BF16 (the operand type of the matrix cores; the error of a
 // term is 2^-9 of it and independent from term to term) into a buffer of one

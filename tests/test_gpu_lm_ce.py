@@ -253,3 +253,48 @@ def test_autograd_stream_and_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(out, ref)), rep
         both()
+
+
+def test_rows_that_do_not_count_may_hold_anything():
+    """NaN and infinite hidden rows of tokens that take no part reach neither gradient."""
+    say("[ce] bad rows that do not count")
+    for n, v in ((10, 300), (200, 300), (700, 1000)):
+        a = make(n, 64, v, 16)
+        good = {k: t.clone() for k, t in a.items()}
+        a["t"][2::5] = -1
+        good["t"][2::5] = -1
+        a["h"][2::5] = float("nan")
+        a["h"][2] = float("inf")
+        lse = lm.linear_ce_fwd(good["h"], good["w"], good["t"])[1]
+        want = lm.linear_ce_bwd(good["h"], good["w"], good["t"], lse, good["dloss"])
+        lse = lm.linear_ce_fwd(a["h"], a["w"], a["t"])[1]
+        got = lm.linear_ce_bwd(a["h"], a["w"], a["t"], lse, a["dloss"])
+        assert torch.equal(got["dh"], want["dh"]) and torch.equal(got["dw"], want["dw"])
+
+
+@pytest.mark.parametrize("n,d,v", [(1500, 64, 700), (3000, 136, 260), (2200, 512, 2000)])
+@pytest.mark.parametrize("kept", [0.0, 0.01, 0.5])
+def test_most_tokens_do_not_count(n, d, v, kept):
+    say(f"[ce] {kept} of the tokens count n={n}")
+    a = make(n, d, v, 17)
+    a["t"][torch.rand(n, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2)) >= kept] = -100
+    check(a, cap=20.0 if n % 4 else 0.0)
+
+
+def test_weights_that_are_zero():
+    """A token whose dloss is zero takes part through dlse alone, and one with neither gives exact zeros."""
+    say("[ce] zero weights")
+    a = make(300, 72, 500, 18)
+    a["dloss"][::2] = 0.0
+    a["dlse"][::3] = 0.0
+    check(a, zloss=True)
+    lse = lm.linear_ce_fwd(a["h"], a["w"], a["t"])[1]
+    g = lm.linear_ce_bwd(a["h"], a["w"], a["t"], lse, a["dloss"], a["dlse"])
+    assert bool((g["dh"][::6] == 0).all()) and bool((g["dh"][1::6] != 0).any(1).all())
+
+
+def test_lists_longer_than_a_workgroup_pass():
+    """More tokens than one pass of the listing workgroup, in one chunk and in several."""
+    say("[ce] long lists")
+    for n, d, v in ((5000, 64, 300), (9000, 64, 15000)):
+        check(make(n, d, v, 19), zloss=n == 9000)
