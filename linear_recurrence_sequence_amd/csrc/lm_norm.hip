@@ -19,6 +19,8 @@
 // every load of a wave covers whole lines.  With W = 1 a workgroup holds four
 // rows and needs no barrier.  Workgroups walk over rows with the weights in
 // registers, and the backward keeps its column sums there until the end.
+// 32768 x 2560, FP32 stream and BF16 branch with a gate: forward 221 us, 5.3 TB/s;
+// backward 322 us, 5.7 TB/s (a large copy runs at 4.7 TB/s).
 #include "lm.hpp"
 
 namespace lrs {
@@ -301,20 +303,26 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void norm_bwd_kernel(const NormAr
     }
 }
 
-// Column sums over the workgroups' partials, FP64 in a fixed order: 32
-// columns a workgroup, 32 lanes down each column.  blockIdx.y: dw_pre, or S
-// and from it dw_post and dscale.
+// Column sums over the workgroups' partials, FP64 in a fixed order: 16
+// columns a workgroup, 64 lanes down each column, eight loads of a lane at a
+// time.  blockIdx.y: dw_pre, or S and from it dw_post and dscale.
 __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* part, int blocks, int d, const float* w_post,
                                                            const float* scale, float* dw_post, float* dscale,
                                                            float* dw_pre) {
-    __shared__ double buf[32][33];
-    const int c = threadIdx.x & 31, lane = threadIdx.x >> 5, col = blockIdx.x * 32 + c, k = blockIdx.y;
+    __shared__ double buf[64][17];
+    const int c = threadIdx.x & 15, lane = threadIdx.x >> 4, col = blockIdx.x * 16 + c, k = blockIdx.y;
     double s = 0.0;
     if (col < d)
-        for (int i = lane; i < blocks; i += 32) s += (double)part[((int64_t)i * 2 + k) * d + col];
+        for (int i = lane; i < blocks; i += 64 * 8) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = i + 64 * u < blocks ? part[((int64_t)(i + 64 * u) * 2 + k) * d + col] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s += (double)v[u];
+        }
     buf[lane][c] = s;
     __syncthreads();
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = 32; o > 0; o >>= 1) {
         if (lane < o) buf[lane][c] += buf[lane + o][c];
         __syncthreads();
     }
@@ -331,14 +339,18 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* part, in
 
 // Waves of a row: NV groups of 256 columns a wave.  Few rows leave the chip
 // idle however they are spread, so they take one group a lane (the shortest
-// chain of loads and sums); many rows take two (four above 8192 columns, where
-// a row would not fit the 16 waves of a workgroup).
+// chain of loads and sums).  Of many rows, those up to 1024 columns are one
+// wave's: four rows are then in flight in a workgroup and no barrier stands
+// between them (backward of 4096 x 1024 bf16: 23 us, 31 us with two waves a row;
+// of 32768 x 1024: 103 us, 112 us).  Wider ones take two groups a wave, four above 8192
+// columns, where a row would not fit the 16 waves of a workgroup.
 struct Plan {
     int nv, waves;
 };
 Plan plan(int64_t rows, int d) {
     const int groups = (int)ceil_div(d, 256);
     if (rows <= 512 && groups <= MAX_WAVES) return {1, groups};
+    if (groups > 2 && groups <= 4) return {4, 1};
     if (groups <= 2 * MAX_WAVES) return {2, (int)ceil_div(groups, 2)};
     return {4, (int)ceil_div(groups, 4)};
 }
@@ -360,7 +372,8 @@ void launch_typed(const NormArgs& a, int blocks, hipStream_t s) {
     const dim3 g(blocks), b(p.waves == 1 ? 256 : 64 * p.waves);
     if (p.waves == 1) {
         if (p.nv == 1) launch_one<BWD, ST, BR, 1, true>(a, g, b, s);
-        else launch_one<BWD, ST, BR, 2, true>(a, g, b, s);
+        else if (p.nv == 2) launch_one<BWD, ST, BR, 2, true>(a, g, b, s);
+        else launch_one<BWD, ST, BR, 4, true>(a, g, b, s);
     } else {
         if (p.nv == 1) launch_one<BWD, ST, BR, 1, false>(a, g, b, s);
         else if (p.nv == 2) launch_one<BWD, ST, BR, 2, false>(a, g, b, s);
@@ -381,14 +394,20 @@ void launch_any(const NormArgs& a, int stream_f32, int branch_f32, int blocks, h
 
 }  // namespace
 
+// Workgroups that walk over the rows.  Each writes its column sums, and HBM
+// serves few long streams better than many: with 5 waves a row (32768 x 2560)
+// 512 workgroups take 322 us, 256 478, 768 380, 1024 410; with 16 (4096 x 8192)
+// 256 take 153 us, 512 165; with 2 (8192 x 1024) 1024 took 47 us, 512 55.
 int lm_norm_bwd_blocks(int64_t rows, int d) {
-    const int per = plan(rows, d).waves == 1 ? 4 : 1;
-    return (int)std::min<int64_t>(ceil_div(rows, per), 1024);
+    const int waves = plan(rows, d).waves, per = waves == 1 ? 4 : 1;
+    return (int)std::min<int64_t>(ceil_div(rows, per), waves > 8 ? 256 : waves >= 4 || waves == 1 ? 512 : 1024);
 }
 
+// The forward keeps nothing between rows; only the widest rows gain from
+// fewer workgroups (4096 x 8192: 768 take 87 us, 4096 100; 32768 x 2560: 221 us either way).
 hipError_t launch_norm_fwd(const NormArgs& a, int stream_f32, int branch_f32, hipStream_t s) {
-    const int per = plan(a.rows, a.d).waves == 1 ? 4 : 1;
-    launch_any<false>(a, stream_f32, branch_f32, (int)std::min<int64_t>(ceil_div(a.rows, per), 4096), s);
+    const int waves = plan(a.rows, a.d).waves, per = waves == 1 ? 4 : 1;
+    launch_any<false>(a, stream_f32, branch_f32, (int)std::min<int64_t>(ceil_div(a.rows, per), waves > 8 ? 768 : 4096), s);
     return hipGetLastError();
 }
 
@@ -396,7 +415,7 @@ hipError_t launch_norm_bwd(const NormArgs& a, int stream_f32, int branch_f32, fl
                            float* dw_pre, hipStream_t s) {
     const int blocks = a.rows ? lm_norm_bwd_blocks(a.rows, a.d) : 0;
     if (blocks) launch_any<true>(a, stream_f32, branch_f32, blocks, s);
-    LRS_LAUNCH(K_LM_NORM_REDUCE, norm_reduce_kernel, dim3((unsigned)ceil_div(a.d, 32), a.w_post ? 2 : 1), dim3(1024), 0, s,
+    LRS_LAUNCH(K_LM_NORM_REDUCE, norm_reduce_kernel, dim3((unsigned)ceil_div(a.d, 16), a.w_post ? 2 : 1), dim3(1024), 0, s,
                (const float*)a.part, blocks, a.d, a.w_post, a.scale, dw_post, dscale, dw_pre);
     return hipGetLastError();
 }

@@ -235,3 +235,13 @@ def test_autograd_stream_and_graph():
         for k in want[2]:
             assert torch.equal(out[2][k], want[2][k]), (rep, k)
         both(a, "silu")
+
+
+@pytest.mark.parametrize("rows,d", [(513, 513), (1030, 770), (600, 1023), (2500, 1024), (700, 1021), (1200, 1025), (300, 6145)])
+@pytest.mark.parametrize("st,br", [(bf, bf), (f32, f32)], ids=["bb", "ff"])
+def test_a_wave_a_row(rows, d, st, br):
+    """Widths around the border between one wave and several a row, with rows to spare and without."""
+    say(f"[norm] wave a row {rows}x{d} {st}")
+    act = ("silu", "sigmoid", "none")[rows % 3]
+    a = make(rows, d, st, br, act, d % 2 == 0, rows + d)
+    check(a, act, both(a, act), plain(a, act))
