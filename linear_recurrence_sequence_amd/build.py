@@ -1,9 +1,10 @@
-"""Build libsamu_scan.so (gfx950) in-tree with hipcc.
+"""Build libsamu_scan.so (gfx950) in-tree with hipcc, and _lm_bind.so with g++.
 
     python -m linear_recurrence_sequence_amd.build [-v]
 
 Every HIP source under csrc/ is compiled for gfx950 only, with packed FP32
 instructions disabled, then linked into one shared library next to this file.
+The binding module links to it and to torch, and is found by its place.
 """
 import concurrent.futures as cf
 import os
@@ -17,6 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libsamu_scan.so")
+BIND = os.path.join(HERE, "_lm_bind.so")
 ARCH = "gfx950"
 
 SOURCES = ["capi.cpp", "prefix.hip", "samu_fwd.hip", "samu_bwd.hip", "samu_decode.hip", "rglru.hip", "baseline.hip", "gate_proj.hip", "noalloc.hip",
@@ -53,6 +55,25 @@ def _compile(src, verbose):
     return obj
 
 
+def _bind(verbose):
+    """The Python module of the language-model operators' usual calls (host code)."""
+    import sysconfig
+
+    import torch
+    at = os.path.dirname(torch.__file__)
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", os.path.join(CSRC, "lm_bind.cpp"), "-o", BIND + ".tmp",
+           f"-I{INCLUDE}", f"-I{at}/include", "-I" + sysconfig.get_paths()["include"],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-L{HERE}", "-l:" + os.path.basename(LIB), f"-L{at}/lib", "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on lm_bind.cpp:\n{r.stderr}")
+    os.replace(BIND + ".tmp", BIND)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     jobs = min(len(SOURCES), max(1, min(8, os.cpu_count() or 1)))
@@ -64,6 +85,7 @@ def build(verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    _bind(verbose)
     return LIB
 
 

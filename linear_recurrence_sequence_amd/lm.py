@@ -6,6 +6,10 @@ linear head, and the AdamW step over many tensors.  Argument checks and
 marshalling only: every step runs in the HIP kernels of libsamu_scan.so, on
 the current stream or the one given.  The differentiable forms are in
 autograd.py.
+
+A plainly right call with outputs of its own goes through _lm_bind (see
+csrc/lm_bind.cpp), which makes the checks below in a few microseconds; every other call is
+checked, and where it is wrong refused, here.
 """
 import ctypes
 
@@ -20,6 +24,18 @@ GATES = {"none": 0, "sigmoid": 1, "silu": 2}
 ADAMW_BLOCK = 256
 
 _lib = None
+_bound = None
+
+
+def _native():
+    """The module behind the usual calls (raises if it has not been built)."""
+    global _bound
+    if _bound is None:
+        scan.lib()
+        from . import _lm_bind
+        _lm_bind.setup(torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        _bound = _lm_bind
+    return _bound
 
 
 def lib():
@@ -125,6 +141,12 @@ def block_norm_fwd(x, y, gate, w_post, scale, w_pre, *, eps=1e-6, gate_act="none
     branch); rows may lie apart (views of a wider projection).  gate_act is
     "none" (gate None), "sigmoid" or "silu"; weights are FP32 [d].  r may be x
     itself.  Returns (r [stream dtype], n [branch dtype], stats f32 [rows, 2])."""
+    if r is None and n is None and stats is None and gate_act in GATES:
+        out = _native().block_norm_fwd(x, y, gate, w_post, scale, w_pre, eps, GATES[gate_act], stream)
+        if out.__class__ is tuple:
+            return out
+        if out is not None:
+            _check(out, "lm_block_norm_fwd")
     rows, d, sx, sy, sg = _norm_args(x, y, gate, w_post, scale, w_pre, gate_act)
     dev = x.device
     if r is None:
@@ -156,6 +178,12 @@ def block_norm_bwd(x, y, gate, w_post, scale, w_pre, stats, dr, dn, *, eps=1e-6,
     and dn (of n, branch dtype); either may be None (zero).  stats are the
     forward's (they hold eps's part).  Returns dict(dx, dy, dgate, dw_post,
     dscale, dw_pre) without the keys of arguments that are None."""
+    if workspace is None and gate_act in GATES:
+        out = _native().block_norm_bwd(x, y, gate, w_post, scale, w_pre, stats, dr, dn, GATES[gate_act], stream)
+        if out.__class__ is dict:
+            return out
+        if out is not None:
+            _check(out, "lm_block_norm_bwd")
     rows, d, sx, sy, sg = _norm_args(x, y, gate, w_post, scale, w_pre, gate_act)
     _want(stats, "stats", _F32, (rows, 2))
     _dense(stats, "stats")
@@ -213,6 +241,12 @@ def linear_ce_fwd(h, w, target, *, softcap=0.0, loss=None, lse=None, workspace=N
     h [..., d] BF16 (rows may lie apart, 16-byte aligned), w [v, d] BF16, target
     [...] int64; a negative target does not count (loss 0).  Returns (loss, lse)
     FP32 [...]."""
+    if loss is None and lse is None and workspace is None:
+        out = _native().linear_ce_fwd(h, w, target, softcap, stream)
+        if out.__class__ is tuple:
+            return out
+        if out is not None:
+            _check(out, "lm_linear_ce_fwd")
     n, d, v, sh = _ce_args(h, w, target)
     dev = h.device
     out = []
@@ -236,6 +270,12 @@ def linear_ce_bwd(h, w, target, lse, dloss, dlse=None, *, softcap=0.0, grad_dtyp
     """Gradients of linear_ce_fwd for the cotangents dloss and dlse (FP32, as
     the target; dlse None = 0), from its lse.  Returns dict(dh, dw) of
     grad_dtype."""
+    if dh is None and dw is None and workspace is None and grad_dtype in _DTYPES:
+        out = _native().linear_ce_bwd(h, w, target, lse, dloss, dlse, softcap, grad_dtype is _F32, stream)
+        if out.__class__ is dict:
+            return out
+        if out is not None:
+            _check(out, "lm_linear_ce_bwd")
     n, d, v, sh = _ce_args(h, w, target)
     dev = h.device
     for t, name in ((lse, "lse"), (dloss, "dloss"), (dlse, "dlse")):
@@ -281,6 +321,10 @@ def adamw_step(params, grads, m, v, *, step, lr, betas=(0.9, 0.999), eps=1e-8, w
     square root (see adamw_state).  masters: FP32 weights of which params are
     the rounded copies.  weight_decay: a number, or one a tensor.  step counts
     from 1; it and lr are taken by value, so a captured graph repeats them."""
+    st = _native().adamw_step(params, grads, m, v, masters, m_scales, v_scales, weight_decay, step, lr, betas[0], betas[1], eps, stream)
+    if st is not None:
+        _check(st, "lm_adamw_step")
+        return
     count = len(params)
     decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * count
     if len(decay) != count:
