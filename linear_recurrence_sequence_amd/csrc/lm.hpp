@@ -138,15 +138,17 @@ struct CeArgs {
     int *list, *place;          // [n] their numbers; place in the list, -1 of the others
     CeToken* token;             // [active]
     void* packed;               // bf16 [active, d] their rows of h
-    void* dz;                   // bf16 [active, chunk]
+    void* dz;                   // bf16 [active, chunk], or [chunk, few]
     float* dh_part;             // [splits, n, d], rows as listed
     void *dh, *dw;
     int grad_f32;
+    int few;                    // columns of dz laid out [chunk, few]; 0: [active, chunk]
 };
 struct CePlan {
     int chunk;   // vocabulary entries a backward pass takes at a time (a multiple of 256)
     int splits;  // ranges of a chunk summed apart for dh
     int dz, dh, dw;  // tile shapes of the three products
+    int few;     // columns of a transposed dz (32, 64, 128 or 256), 0 with many tokens
 };
 int ce_parts(int n, int d, int v);
 CePlan ce_plan(int n, int d, int v);

@@ -106,7 +106,7 @@ size_t ce_layout(bool bwd, int n, int d, int v, void* base, CeArgs* a) {
         a->place = static_cast<int*>(take((size_t)n * 4));
         a->token = static_cast<CeToken*>(take((size_t)n * sizeof(CeToken)));
         a->packed = take((size_t)n * d * 2);
-        a->dz = take((size_t)n * pl.chunk * 2);
+        a->dz = take((size_t)(pl.few ? pl.few : n) * pl.chunk * 2);
         a->dh_part = static_cast<float*>(take((size_t)pl.splits * n * d * 4));
     } else {
         a->part = static_cast<float*>(take((size_t)ce_parts(n, d, v) * n * 8));

@@ -162,17 +162,27 @@ __device__ __forceinline__ void token_weights(const CeArgs& a, int tok, float* d
     *c = a.dlse ? *dl + a.dlse[tok] : *dl;
 }
 
+// Row `from` of h to row `to` of the packed ones, by one wave.
+__device__ __forceinline__ void pack_row(const CeArgs& a, int from, int to) {
+    const u32x4_t* p = reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.h) + from * a.h_stride);
+    u32x4_t* o = reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.packed) + (int64_t)to * a.d);
+    for (int i = threadIdx.x & 63; i < a.d / 8; i += 64) o[i] = p[i];
+}
+constexpr int LIST_PACKS = 1024;  // tokens up to which the listing launch packs
+
 // Lists the tokens that take part, those with a weight, in their order; the
 // products run over these alone, so prompt and padding tokens cost nothing and
 // whatever their rows hold stays out of dw.  Also the scale that dz is held at, the
 // largest |dloss| or |dloss + dlse|: BF16 rounds dloss itself, and where all tokens
 // weigh the same it would round each target's entry the same way, an error that no
 // sum averages out; over the scale those entries are 1 - p.  Both products
-// give it back.  One workgroup.
+// give it back.  One workgroup; up to 1024 tokens, a workgroup for 16 packed rows, each
+// of which makes the list for itself and packs its rows (a launch less).
 __global__ __launch_bounds__(1024) void ce_list_kernel(const CeArgs a) {
     __shared__ float best[16];
-    __shared__ int count[16];
+    __shared__ int count[16], source[16];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const bool writes = blockIdx.x == 0, packs = a.n <= LIST_PACKS;
     float top = 0.0f;
     for (int i = threadIdx.x; i < a.n; i += 1024) {
         float dl, c;
@@ -204,6 +214,8 @@ __global__ __launch_bounds__(1024) void ce_list_kernel(const CeArgs a) {
         done += all;
         if (i < a.n) {
             const int at = in ? before + __popcll(some & ((1ull << lane) - 1)) : -1;
+            if (packs && in && at >> 4 == (int)blockIdx.x) source[at & 15] = i;
+            if (!writes) continue;
             a.place[i] = at;
             if (in) {
                 const int64_t y = a.target[i];
@@ -212,29 +224,30 @@ __global__ __launch_bounds__(1024) void ce_list_kernel(const CeArgs a) {
             }
         }
     }
-    if (threadIdx.x == 0) {
+    if (writes && threadIdx.x == 0) {
         *a.scale = scale;
         *a.active = done;
     }
+    __syncthreads();
+    const int row = (int)blockIdx.x * 16 + wave;
+    if (packs && row < done) pack_row(a, source[wave], row);
 }
 
-// Rows of h that take part, packed: a wave a row, 8 elements a lane at a time.
+// Rows of h that take part, packed: a wave a row.
 __global__ __launch_bounds__(256) void ce_pack_kernel(const CeArgs a) {
-    const int row = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    if (row >= *a.active) return;
-    const u32x4_t* from = reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.h) + a.list[row] * a.h_stride);
-    u32x4_t* to = reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.packed) + (int64_t)row * a.d);
-    for (int i = lane; i < a.d / 8; i += 64) to[i] = from[i];
+    const int row = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row < *a.active) pack_row(a, a.list[row], row);
 }
 
 // dz / scale of vocabulary entries [vfirst, vfirst + count) for the listed tokens, BF16 [active, ld];
-// columns from count to the next multiple of 64 are zeros.
+// columns from count to the next multiple of 64 are zeros.  With few tokens (a.few > 0)
+// it is laid out [count, few], zeros beyond the listed tokens.
 template <class T, bool CAP>
 __global__ __launch_bounds__(T::THREADS) void ce_dz_kernel(const CeArgs a, int np, int vfirst, int count, int ld) {
     __shared__ __attribute__((aligned(1024))) char lds[T::LDS_BYTES];
     __shared__ CeToken token[T::TILE_Q];
     constexpr int BM = T::TILE_P, BN = T::TILE_Q;
-    const int m = *a.active, nq = (m + BN - 1) / BN;
+    const int m = *a.active, nq = ((a.few ? a.few : m) + BN - 1) / BN;
     if ((int)blockIdx.x >= np * nq) return;
     int tp, tq;
     tile_of(np, nq, blockIdx.x, &tp, &tq);
@@ -258,8 +271,8 @@ __global__ __launch_bounds__(T::THREADS) void ce_dz_kernel(const CeArgs a, int n
 #pragma unroll
     for (int j = 0; j < T::FN; ++j) {
         const int tok = tq * BN + T::row_q(j) + (lane & 15);
-        if (tok >= m) continue;
-        const CeToken k = token[T::row_q(j) + (lane & 15)];
+        if (tok >= (a.few ? a.few : m)) continue;
+        const CeToken k = tok < m ? token[T::row_q(j) + (lane & 15)] : CeToken{0.0f, 0.0f, 0.0f, -1};
         const int y = k.target - vfirst - v0;  // no row of this wave where there is no target: rows + v0 + vfirst is not negative
         uint16_t* out = static_cast<uint16_t*>(a.dz) + (int64_t)tok * ld + v0;
 #pragma unroll
@@ -277,14 +290,21 @@ __global__ __launch_bounds__(T::THREADS) void ce_dz_kernel(const CeArgs a, int n
                 if (y == T::row_p(i) + r) g[r] -= k.dl;
                 if (CAP) g[r] *= slope;
             }
-            if (!edge || v0 + T::row_p(i) < padded)
+            if (a.few) {
+                if (tok >= m) g[0] = g[1] = g[2] = g[3] = 0.0f;
+                uint16_t* t16 = static_cast<uint16_t*>(a.dz) + (int64_t)(v0 + T::row_p(i)) * a.few + tok;
+                const uint32_t lo = pack_bf16x2(g[0], g[1]), hi = pack_bf16x2(g[2], g[3]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (!edge || v0 + T::row_p(i) + r < count) t16[r * a.few] = (uint16_t)((r < 2 ? lo : hi) >> (16 * (r & 1)));
+            } else if (!edge || v0 + T::row_p(i) < padded)
                 *reinterpret_cast<u32x2_t*>(out + T::row_p(i)) = u32x2_t{pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3])};
         }
     }
 }
 
 // dh_part[s] (+)= dz w_chunk over range s of the chunk.  P = w (width; the
-// reduction index is not the dense one), Q = dz.
+// reduction index is not the dense one), Q = dz (dense in it but with few tokens).
 template <class T>
 __global__ __launch_bounds__(T::THREADS) void ce_dh_kernel(const CeArgs a, int np, int vfirst, int count, int ld, int range,
                                                            int splits, int first) {
@@ -297,7 +317,7 @@ __global__ __launch_bounds__(T::THREADS) void ce_dh_kernel(const CeArgs a, int n
     const int split = blockIdx.x / tiles, k0 = split * range, k1 = k0 + range < count ? k0 + range : count;
     float* out = a.dh_part + (int64_t)split * a.n * a.d;
     T t;
-    t.run(lds, Operand{static_cast<const char*>(a.w) + (int64_t)vfirst * a.d * 2, a.d, a.d}, Operand{a.dz, ld, m}, tp * BM,
+    t.run(lds, Operand{static_cast<const char*>(a.w) + (int64_t)vfirst * a.d * 2, a.d, a.d}, a.few ? Operand{a.dz, a.few, a.few} : Operand{a.dz, ld, m}, tp * BM,
           tq * BN, k0, k1);
     const int lane = threadIdx.x & 63;
     const int c0 = tp * BM + 4 * (lane >> 4), t0 = tq * BN + (lane & 15);
@@ -315,26 +335,34 @@ __global__ __launch_bounds__(T::THREADS) void ce_dh_kernel(const CeArgs a, int n
     }
 }
 
-// dh from the ranges' sums; zeros for the tokens that take no part.  A wave a row.
+// dh from the ranges' sums; zeros for the tokens that take no part.  Four
+// columns a lane; of many ranges, G lanes sum every G-th each.
+template <int G>
 __global__ __launch_bounds__(256) void ce_dh_join_kernel(const CeArgs a, int splits) {
-    const int row = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    if (row >= a.n) return;
-    const int at = a.place[row];
-    const float scale = *a.scale;
-    const int64_t part = (int64_t)a.n * a.d / 4;
-    const f32acc_t* from = reinterpret_cast<const f32acc_t*>(a.dh_part) + (int64_t)at * (a.d / 4);
-    for (int i = lane; i < a.d / 4; i += 64) {
-        f32acc_t s = {0.f, 0.f, 0.f, 0.f};
+    constexpr int WIDE = 256 / G;
+    __shared__ f32acc_t buf[G][WIDE];
+    const int64_t part = (int64_t)a.n * a.d / 4, i = (int64_t)blockIdx.x * WIDE + threadIdx.x % WIDE;
+    const int g = threadIdx.x / WIDE, line = a.d / 4;
+    f32acc_t s = {0.f, 0.f, 0.f, 0.f};
+    if (i < part) {
+        const int at = a.place[i / line];
         if (at >= 0) {
-            s = from[i];
+            const f32acc_t* from = reinterpret_cast<const f32acc_t*>(a.dh_part) + (int64_t)at * line + i % line;
 #pragma unroll 8
-            for (int k = 1; k < splits; ++k) s += from[i + k * part];
-            s *= scale;
+            for (int k = g; k < splits; k += G) s += from[k * part];
+            s *= *a.scale;
         }
-        const int64_t o = (int64_t)row * (a.d / 4) + i;
-        if (a.grad_f32) reinterpret_cast<f32acc_t*>(a.dh)[o] = s;
-        else reinterpret_cast<u32x2_t*>(a.dh)[o] = u32x2_t{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
     }
+    if (G > 1) {
+        buf[g][threadIdx.x % WIDE] = s;
+        __syncthreads();
+        if (g > 0) return;
+#pragma unroll
+        for (int k = 1; k < G; ++k) s += buf[k][threadIdx.x];
+    }
+    if (i >= part) return;
+    if (a.grad_f32) reinterpret_cast<f32acc_t*>(a.dh)[i] = s;
+    else reinterpret_cast<u32x2_t*>(a.dh)[i] = u32x2_t{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
 }
 
 // dw of a chunk = dz^T h.  P = h (width), Q = dz (vocabulary); tokens are the
@@ -366,6 +394,112 @@ __global__ __launch_bounds__(T::THREADS) void ce_dw_kernel(const CeArgs a, int n
     }
 }
 
+// dw of a chunk with few tokens (at most 32 KS): bound by writing dw.  A wave
+// keeps the fragments of 64 columns of h in registers and walks over the
+// vocabulary.  The workgroup's rows of dz, [count, 32 KS], are 8 KiB in a row: they are
+// loaded as they lie, one piece ahead, and the fragments read from LDS (a fragment read
+// from memory takes a line a lane: 70 us of the 108 us that 128 tokens x 2048 x 65536
+// took).  The column
+// of result r of fragment f in lane group g is chosen so that a lane's results of two
+// fragments are 16 bytes of a row: 32 (f / 2) + 8 g + 4 (f % 2) + r.
+template <int KS>
+__global__ __launch_bounds__(256) void ce_dw_few_kernel(const CeArgs a, int vfirst, int count) {
+    constexpr int U = 8 / KS, ROWS = U * 16, PIECES = KS * 4, PITCH = KS * 64 + 16;
+    constexpr int LINE = 512 + 16;  // of 32 tokens' 256 columns of h, which stand in the same place first
+    __shared__ __attribute__((aligned(16))) char lds[2 * ROWS * PITCH];
+    static_assert(32 * LINE <= 2 * ROWS * PITCH, "32 tokens fit");
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, m = *a.active;
+    // an XCD writes whole rows: its workgroups take the columns of the same rows of dz
+    const int cols = (a.d + 255) / 256, on = blockIdx.x >> 3, b0 = on % cols * 256, c0 = b0 + wave * 64;
+    const int first = ((on / cols) * 8 + (blockIdx.x & 7)) * ROWS, stride = (int)gridDim.x / cols * ROWS;
+    const float scale = *a.scale;
+    bf16x8_t p[4][KS];
+    u32x4_t slab[4];
+    const auto fetch = [&](int ks) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = i * 256 + threadIdx.x, tok = ks * 32 + at / 32, c = b0 + at % 32 * 8;
+            slab[i] = tok < m && c < a.d ? *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.packed) + (int64_t)tok * a.d + c)
+                                         : u32x4_t{0u, 0u, 0u, 0u};
+        }
+    };
+    fetch(0);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = i * 256 + threadIdx.x;
+            *reinterpret_cast<u32x4_t*>(lds + at / 32 * LINE + at % 32 * 16) = slab[i];
+        }
+        lds_barrier();
+        if (ks + 1 < KS) fetch(ks + 1);
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            // the transposing read: lane s of 16 reads 4 columns of one of 4 tokens and receives its own
+            // column of all four; its own is the s % 4-th of the s / 4-th such four
+            typedef __attribute__((address_space(3))) s16x4_t lds4;
+            const int s = lane & 15, tok = 8 * g + (s >> 2), c = wave * 64 + 32 * (f / 2) + 8 * (s & 3) + 4 * (f % 2);
+            const char* from = lds + tok * LINE + c * 2;
+            s16x4_t v[2];
+            v[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)from);
+            v[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(from + 4 * LINE));
+            p[f][ks] = __builtin_bit_cast(bf16x8_t, v);
+        }
+        lds_barrier();
+    }
+    const u32x4_t* dz = static_cast<const u32x4_t*>(a.dz);
+    u32x4_t x[2];
+    const auto load = [&](int row) {  // rows beyond the last are read as the last, and not stored
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = i * 256 + threadIdx.x, r = row + at / PIECES;
+            x[i] = dz[(int64_t)(r < count ? r : count - 1) * PIECES + at % PIECES];
+        }
+    };
+    const auto store = [&](const char* from, int row, bool whole) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int v = row + u * 16 + (lane & 15);
+            f32acc_t c[4] = {};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                const bf16x8_t q = *reinterpret_cast<const bf16x8_t*>(from + (u * 16 + (lane & 15)) * PITCH + (ks * 4 + g) * 16);
+#pragma unroll
+                for (int f = 0; f < 4; ++f) c[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(p[f][ks], q, c[f], 0, 0, 0);
+            }
+            if (!whole && v >= count) continue;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int col = c0 + 32 * h + 8 * g;
+                if (!whole && col >= a.d) continue;
+                const f32acc_t y = c[2 * h] * scale, z = c[2 * h + 1] * scale;
+                const int64_t at = (int64_t)(vfirst + v) * a.d + col;
+                if (a.grad_f32) {
+                    f32acc_t* o = reinterpret_cast<f32acc_t*>(static_cast<float*>(a.dw) + at);
+                    o[0] = y;
+                    o[1] = z;
+                } else {
+                    *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.dw) + at) =
+                        u32x4_t{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3])};
+                }
+            }
+        }
+    };
+    load(first);
+    int b = 0;
+    for (int row = first; row < count; row += stride, b ^= 1) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = i * 256 + threadIdx.x;
+            *reinterpret_cast<u32x4_t*>(lds + b * (ROWS * PITCH) + at / PIECES * PITCH + at % PIECES * 16) = x[i];
+        }
+        lds_barrier();
+        load(row + stride);
+        if (row + ROWS <= count && c0 + 64 <= a.d) store(lds + b * (ROWS * PITCH), row, true);
+        else store(lds + b * (ROWS * PITCH), row, false);
+    }
+}
+
 __global__ __launch_bounds__(256) void ce_zero_kernel(uint32_t* p, int64_t words) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i < words) p[i] = 0u;
@@ -387,6 +521,7 @@ using Few = ThinProduct<64, 32, 4, 1, PT, QT>;
 enum Shape { LARGE, SMALL, FEW };
 constexpr int kBM[3] = {256, 128, 64}, kBN[3] = {256, 128, 32};
 
+constexpr int kFew = 256;  // tokens up to which the backward goes by the bytes of w and dw
 constexpr int64_t kMostDz = (int64_t)128 << 20;  // elements of dz held at once
 
 // Time of a product of p x q results over k, in microseconds: rounds of
@@ -413,6 +548,18 @@ int ce_parts(int n, int d, int v) { return (int)ceil_div(v, kBM[stats_shape(n, d
 // counts from the least that the buffer of dz allows.
 CePlan ce_plan(int n, int d, int v) {
     n = std::max(n, 1);
+    if (n <= kFew) {
+        CePlan p{};
+        p.few = n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
+        const int64_t chunks = ceil_div(v, kMostDz / p.few / 256 * 256);
+        p.chunk = (int)(ceil_div(ceil_div(v, chunks), 256) * 256);
+        p.dh = n <= 32 ? FEW : SMALL;
+        p.dz = n <= 32 ? FEW : shape_for(std::min(p.chunk, v), n, d);
+        // the product over the vocabulary reads w once: enough ranges to fill the chip, four steps or more each
+        const int64_t tiles = ceil_div(d, kBM[p.dh]) * ceil_div(n, kBN[p.dh]), want = (p.dh == FEW ? 1024 : 512) / tiles;
+        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(want, std::min(p.chunk, v) / (4 * GEMM_BK)));
+        return p;
+    }
     const int64_t most = std::max<int64_t>(256, kMostDz / n / 256 * 256), least = ceil_div(v, most);
     CePlan best{};
     double best_us = 0.0;
@@ -420,14 +567,11 @@ CePlan ce_plan(int n, int d, int v) {
         const int64_t chunk = ceil_div(ceil_div(v, chunks), 256) * 256, count = std::min<int64_t>(chunk, v);
         CePlan p{};
         p.chunk = (int)chunk;
-        p.dz = n <= 32 ? FEW : shape_for(count, n, d);
+        p.dz = shape_for(count, n, d);
         p.dw = shape_for(d, count, n);
-        double us = n <= 32 ? 0.0 : product_us((Shape)p.dz, count, n, d);
-        us += product_us((Shape)p.dw, d, count, n);
-        double dh_us = 0.0;
-        for (int s = LARGE; s <= FEW; ++s) {
-            if ((s == FEW) != (n <= 32)) continue;
-            for (int splits = 1; splits <= 16 && (splits == 1 || count / splits >= 8 * GEMM_BK); ++splits) {
+        double us = product_us((Shape)p.dz, count, n, d) + product_us((Shape)p.dw, d, count, n), dh_us = 0.0;
+        for (int s = LARGE; s <= SMALL; ++s) {
+            for (int splits = 1; splits <= 64 && (splits == 1 || count / splits >= 8 * GEMM_BK); ++splits) {
                 // the partial sums are written, and read by the next chunk or the last launch
                 const double t = product_us((Shape)s, d, (int64_t)n * splits, ceil_div(count, splits)) + (double)splits * n * d * 8 / 4.5e6;
                 if (dh_us == 0.0 || t < dh_us) dh_us = t, p.dh = s, p.splits = splits;
@@ -449,7 +593,6 @@ CePlan ce_plan(int n, int d, int v) {
 #define CE_STATS_CAP(...) ce_stats_kernel<__VA_ARGS__, true>
 #define CE_DZ(...) ce_dz_kernel<__VA_ARGS__, false>
 #define CE_DZ_CAP(...) ce_dz_kernel<__VA_ARGS__, true>
-#define CE_DH(...) ce_dh_kernel<__VA_ARGS__>
 
 hipError_t launch_ce_fwd(const CeArgs& a, hipStream_t s) {
     const Shape sh = stats_shape(a.n, a.d, a.v);
@@ -462,22 +605,27 @@ hipError_t launch_ce_fwd(const CeArgs& a, hipStream_t s) {
 }
 
 // Grids are sized for all tokens; what lies beyond the listed ones exits at once.
-hipError_t launch_ce_bwd(const CeArgs& a, hipStream_t s) {
+hipError_t launch_ce_bwd(const CeArgs& args, hipStream_t s) {
+    CeArgs a = args;
     if (a.n == 0) {  // no token: dw is zero, and there is no dh
         const int64_t words = (int64_t)a.v * a.d * (a.grad_f32 ? 4 : 2) / 4;
         LRS_LAUNCH(K_CLEAR, ce_zero_kernel, dim3((unsigned)ceil_div(words, 256)), dim3(256), 0, s, (uint32_t*)a.dw, words);
         return hipGetLastError();
     }
     const CePlan pl = ce_plan(a.n, a.d, a.v);
-    const dim3 rows((unsigned)ceil_div(a.n, 4));
-    LRS_LAUNCH(K_LM_CE_LIST, ce_list_kernel, dim3(1), dim3(1024), 0, s, a);
-    LRS_LAUNCH(K_LM_CE_LIST, ce_pack_kernel, rows, dim3(256), 0, s, a);
+    a.few = pl.few;
+    if (a.n <= LIST_PACKS) {
+        LRS_LAUNCH(K_LM_CE_LIST, ce_list_kernel, dim3((unsigned)ceil_div(a.n, 16)), dim3(1024), 0, s, a);
+    } else {
+        LRS_LAUNCH(K_LM_CE_LIST, ce_list_kernel, dim3(1), dim3(1024), 0, s, a);
+        LRS_LAUNCH(K_LM_CE_LIST, ce_pack_kernel, dim3((unsigned)ceil_div(a.n, 4)), dim3(256), 0, s, a);
+    }
     int used = 1;  // ranges of the first chunk, which is the longest
     for (int v0 = 0; v0 < a.v; v0 += pl.chunk) {
         const int count = std::min(pl.chunk, a.v - v0), ld = pl.chunk;
         {
             const int np = (int)ceil_div(count, kBM[pl.dz]);
-            const dim3 g((unsigned)(np * ceil_div(a.n, kBN[pl.dz])));
+            const dim3 g((unsigned)(np * ceil_div(pl.few ? pl.few : a.n, kBN[pl.dz])));
             if (a.cap > 0.0f) CE_SHAPES(pl.dz, K_LM_CE_DZ, g, CE_DZ_CAP, Wide, false, false, a, np, v0, count, ld);
             else CE_SHAPES(pl.dz, K_LM_CE_DZ, g, CE_DZ, Wide, false, false, a, np, v0, count, ld);
         }
@@ -486,16 +634,28 @@ hipError_t launch_ce_bwd(const CeArgs& a, hipStream_t s) {
             const int range = (int)(ceil_div(ceil_div(count, pl.splits), GEMM_BK) * GEMM_BK), splits = (int)ceil_div(count, range);
             if (v0 == 0) used = splits;
             const dim3 g((unsigned)(np * ceil_div(a.n, kBN[pl.dh]) * splits));
-            CE_SHAPES(pl.dh, K_LM_CE_DH, g, CE_DH, Large, true, false, a, np, v0, count, ld, range, splits, v0 == 0);
+            if (pl.dh == LARGE) LRS_LAUNCH(K_LM_CE_DH, (ce_dh_kernel<Large<true, false>>), g, dim3(Large<true, false>::THREADS), 0, s, a, np, v0, count, ld, range, splits, v0 == 0);
+            else if (!pl.few) LRS_LAUNCH(K_LM_CE_DH, (ce_dh_kernel<Small<true, false>>), g, dim3(Small<true, false>::THREADS), 0, s, a, np, v0, count, ld, range, splits, v0 == 0);
+            else if (pl.dh == SMALL) LRS_LAUNCH(K_LM_CE_DH, (ce_dh_kernel<Small<true, true>>), g, dim3(Small<true, true>::THREADS), 0, s, a, np, v0, count, ld, range, splits, v0 == 0);
+            else LRS_LAUNCH(K_LM_CE_DH, (ce_dh_kernel<Few<true, true>>), g, dim3(Few<true, true>::THREADS), 0, s, a, np, v0, count, ld, range, splits, v0 == 0);
         }
-        {
+        if (pl.few) {
+            const int cols = (int)ceil_div(a.d, 256), rows = 4096 / pl.few;  // rows of dz a workgroup takes at a time
+            const dim3 g((unsigned)(cols * 8 * std::max<int64_t>(1, std::min<int64_t>(ceil_div(count, 8 * rows), 64 / cols))));
+            if (pl.few == 32) LRS_LAUNCH(K_LM_CE_DW, ce_dw_few_kernel<1>, g, dim3(256), 0, s, a, v0, count);
+            else if (pl.few == 64) LRS_LAUNCH(K_LM_CE_DW, ce_dw_few_kernel<2>, g, dim3(256), 0, s, a, v0, count);
+            else if (pl.few == 128) LRS_LAUNCH(K_LM_CE_DW, ce_dw_few_kernel<4>, g, dim3(256), 0, s, a, v0, count);
+            else LRS_LAUNCH(K_LM_CE_DW, ce_dw_few_kernel<8>, g, dim3(256), 0, s, a, v0, count);
+        } else {
             const int np = (int)ceil_div(a.d, kBM[pl.dw]), nq = (int)ceil_div(count, kBN[pl.dw]);
             const dim3 g((unsigned)(np * nq));
             if (pl.dw == LARGE) LRS_LAUNCH(K_LM_CE_DW, (ce_dw_kernel<Large<true, true>>), g, dim3(Large<true, true>::THREADS), 0, s, a, np, nq, v0, count, ld);
             else LRS_LAUNCH(K_LM_CE_DW, (ce_dw_kernel<Small<true, true>>), g, dim3(Small<true, true>::THREADS), 0, s, a, np, nq, v0, count, ld);
         }
     }
-    LRS_LAUNCH(K_LM_CE_JOIN, ce_dh_join_kernel, rows, dim3(256), 0, s, a, used);
+    const int64_t quads = (int64_t)a.n * a.d / 4;
+    if (used >= 8) LRS_LAUNCH(K_LM_CE_JOIN, ce_dh_join_kernel<8>, dim3((unsigned)ceil_div(quads, 32)), dim3(256), 0, s, a, used);
+    else LRS_LAUNCH(K_LM_CE_JOIN, ce_dh_join_kernel<1>, dim3((unsigned)ceil_div(quads, 256)), dim3(256), 0, s, a, used);
     return hipGetLastError();
 }
 

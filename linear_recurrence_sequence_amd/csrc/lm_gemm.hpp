@@ -34,6 +34,13 @@ struct Operand {
 
 constexpr int GEMM_BK = 64;
 
+// A barrier for what the workgroup keeps in LDS, which leaves loads and stores in flight.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // BM x BN tile, WM x WN waves; PT / QT: the operand lies as [k][rows].
 template <int BM, int BN, int WM, int WN, bool PT, bool QT>
 struct TileProduct {

@@ -298,3 +298,16 @@ def test_lists_longer_than_a_workgroup_pass():
     say("[ce] long lists")
     for n, d, v in ((5000, 64, 300), (9000, 64, 15000)):
         check(make(n, d, v, 19), zloss=n == 9000)
+
+
+@pytest.mark.parametrize("n", [1, 31, 32, 33, 64, 65, 128, 129, 200, 256, 257])
+@pytest.mark.parametrize("d,v", [(8, 17), (264, 700), (640, 5003)])
+def test_few_tokens(n, d, v):
+    """Around the counts where the layout of the few tokens' dz changes; some, one or no token with a weight."""
+    say(f"[ce] few tokens n={n} d={d} v={v}")
+    a = make(n, d, v, n + d)
+    check(a, cap=15.0 if n % 3 == 0 else 0.0, zloss=n % 2 == 0, grad_dtype=f32 if v % 3 else bf)
+    a["t"][: n - 1] = -1
+    check(a)
+    a["t"].fill_(-1)
+    check(a)
