@@ -10,6 +10,8 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/LegacyTypeDispatch.h>
+#include <ATen/ops/as_strided.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/ScalarType.h>
 #include <torch/csrc/Exceptions.h>
@@ -46,11 +48,19 @@ void* dense(const Tensor& t, at::ScalarType type, const c10::Device& dev) {
     return t.data_ptr();
 }
 
-// Rows of t [..., d] with their distance in elements: dense, or the rows of one matrix.
+// Elements from one row of t [..., d] to the next: rows of dense columns at one distance.
 int64_t row_stride(const Tensor& t) {
-    if (t.is_contiguous()) return t.size(-1);
-    need(t.dim() == 2 && t.stride(1) == 1 && t.size(0) > 1 && t.size(1) > 1);
-    return t.stride(0);
+    const int64_t d = t.size(-1);
+    if (t.is_contiguous()) return d;
+    need(t.stride(-1) == 1 || d == 1);
+    int64_t step = -1, reach = 0;
+    for (int64_t i = t.dim() - 2; i >= 0; --i) {
+        if (t.size(i) == 1) continue;
+        if (step < 0) step = t.stride(i);
+        else need(t.stride(i) == reach);
+        reach = t.stride(i) * t.size(i);
+    }
+    return step < 0 ? d : step;
 }
 
 struct Matrix {
@@ -99,6 +109,7 @@ double number(PyObject* o) {
 template <class F>
 PyObject* guarded(F f) {
     HANDLE_TH_ERRORS
+    at::AutoDispatchBelowADInplaceOrView below;  // what is made here has no gradient of its own
     try {
         return f();
     } catch (const Leave&) {
@@ -186,10 +197,10 @@ PyObject* block_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t count) {
         put(out, "dy", dy);
         if (dg.defined()) put(out, "dgate", dg);
         if (k.w_post) {
-            put(out, "dw_post", dw.select(0, 1).narrow(0, 0, k.d));
-            put(out, "dscale", dw.select(0, 2).narrow(0, 0, k.d));
+            put(out, "dw_post", dw.as_strided({k.d}, {1}, line));
+            put(out, "dscale", dw.as_strided({k.d}, {1}, 2 * line));
         }
-        put(out, "dw_pre", dw.select(0, 0).narrow(0, 0, k.d));
+        put(out, "dw_pre", dw.as_strided({k.d}, {1}, 0));
         return out;
     });
 }

@@ -116,7 +116,8 @@ size_t ce_layout(bool bwd, int n, int d, int v, void* base, CeArgs* a) {
 }
 
 bool ce_shape(int64_t n, int d, int64_t v) {
-    return n >= 0 && n < 0x7fffffff - 512 && v >= 1 && v < 0x7fffffff - 512 && d >= 8 && d <= 65536 && d % 8 == 0;
+    return n >= 0 && n < 0x7fffffff - 512 && v >= 1 && v < 0x7fffffff - 512 && d >= 8 && d <= 65536 && d % 8 == 0 &&
+           ceil_div(n, 128) * ceil_div(v, 128) < 0x7fffffff;  // the smaller tiles of a grid
 }
 
 scan_status ce_check(const char* fn, int64_t n, int d, int64_t v, double cap, int64_t h_stride) {

@@ -7,6 +7,9 @@ marshalling only: every step runs in the HIP kernels of libsamu_scan.so, on
 the current stream or the one given.  The differentiable forms are in
 autograd.py.
 
+With a stream given a call runs as if that stream were the current one: its
+outputs and workspace are allocated there.
+
 A plainly right call with outputs of its own goes through _lm_bind (see
 csrc/lm_bind.cpp), which makes the checks below in a few microseconds; every other call is
 checked, and where it is wrong refused, here.
@@ -141,8 +144,11 @@ def block_norm_fwd(x, y, gate, w_post, scale, w_pre, *, eps=1e-6, gate_act="none
     branch); rows may lie apart (views of a wider projection).  gate_act is
     "none" (gate None), "sigmoid" or "silu"; weights are FP32 [d].  r may be x
     itself.  Returns (r [stream dtype], n [branch dtype], stats f32 [rows, 2])."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return block_norm_fwd(x, y, gate, w_post, scale, w_pre, eps=eps, gate_act=gate_act, r=r, n=n, stats=stats)
     if r is None and n is None and stats is None and gate_act in GATES:
-        out = _native().block_norm_fwd(x, y, gate, w_post, scale, w_pre, eps, GATES[gate_act], stream)
+        out = _native().block_norm_fwd(x, y, gate, w_post, scale, w_pre, eps, GATES[gate_act], None)
         if out.__class__ is tuple:
             return out
         if out is not None:
@@ -167,7 +173,7 @@ def block_norm_fwd(x, y, gate, w_post, scale, w_pre, *, eps=1e-6, gate_act="none
     _same_device(x, r=r, n=n, stats=stats)
     st = lib().lm_block_norm_fwd(rows, d, _code(x.dtype), _code(y.dtype), GATES[gate_act], eps, _p(x),
                                  sx, _p(y), sy, _p(gate), sg, _p(w_post), _p(scale), _p(w_pre), _p(r), _p(n),
-                                 _p(stats), _stream(stream))
+                                 _p(stats), _stream(None))
     _check(st, "lm_block_norm_fwd")
     return r, n, stats
 
@@ -178,8 +184,11 @@ def block_norm_bwd(x, y, gate, w_post, scale, w_pre, stats, dr, dn, *, eps=1e-6,
     and dn (of n, branch dtype); either may be None (zero).  stats are the
     forward's (they hold eps's part).  Returns dict(dx, dy, dgate, dw_post,
     dscale, dw_pre) without the keys of arguments that are None."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return block_norm_bwd(x, y, gate, w_post, scale, w_pre, stats, dr, dn, eps=eps, gate_act=gate_act, workspace=workspace)
     if workspace is None and gate_act in GATES:
-        out = _native().block_norm_bwd(x, y, gate, w_post, scale, w_pre, stats, dr, dn, GATES[gate_act], stream)
+        out = _native().block_norm_bwd(x, y, gate, w_post, scale, w_pre, stats, dr, dn, GATES[gate_act], None)
         if out.__class__ is dict:
             return out
         if out is not None:
@@ -205,7 +214,7 @@ def block_norm_bwd(x, y, gate, w_post, scale, w_pre, stats, dr, dn, *, eps=1e-6,
                                  _p(y), sy, _p(gate), sg, _p(w_post), _p(scale), _p(w_pre), _p(stats), _p(dr),
                                  _row_stride(dr, "dr"), _p(dn), _row_stride(dn, "dn"), _p(out["dx"]), _p(out["dy"]),
                                  _p(out.get("dgate")), _p(out.get("dw_post")), _p(out.get("dscale")),
-                                 _p(out["dw_pre"]), _p(workspace), _nbytes(workspace), _stream(stream))
+                                 _p(out["dw_pre"]), _p(workspace), _nbytes(workspace), _stream(None))
     _check(st, "lm_block_norm_bwd")
     return out
 
@@ -241,8 +250,11 @@ def linear_ce_fwd(h, w, target, *, softcap=0.0, loss=None, lse=None, workspace=N
     h [..., d] BF16 (rows may lie apart, 16-byte aligned), w [v, d] BF16, target
     [...] int64; a negative target does not count (loss 0).  Returns (loss, lse)
     FP32 [...]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_ce_fwd(h, w, target, softcap=softcap, loss=loss, lse=lse, workspace=workspace)
     if loss is None and lse is None and workspace is None:
-        out = _native().linear_ce_fwd(h, w, target, softcap, stream)
+        out = _native().linear_ce_fwd(h, w, target, softcap, None)
         if out.__class__ is tuple:
             return out
         if out is not None:
@@ -260,7 +272,7 @@ def linear_ce_fwd(h, w, target, *, softcap=0.0, loss=None, lse=None, workspace=N
     loss, lse = out
     workspace = _ce_workspace(n, d, v, 0, workspace, dev)
     st = lib().lm_linear_ce_fwd(n, d, v, softcap, _p(h), sh, _p(w), _p(target), _p(loss), _p(lse), _p(workspace),
-                                _nbytes(workspace), _stream(stream))
+                                _nbytes(workspace), _stream(None))
     _check(st, "lm_linear_ce_fwd")
     return loss, lse
 
@@ -270,8 +282,11 @@ def linear_ce_bwd(h, w, target, lse, dloss, dlse=None, *, softcap=0.0, grad_dtyp
     """Gradients of linear_ce_fwd for the cotangents dloss and dlse (FP32, as
     the target; dlse None = 0), from its lse.  Returns dict(dh, dw) of
     grad_dtype."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return linear_ce_bwd(h, w, target, lse, dloss, dlse, softcap=softcap, grad_dtype=grad_dtype, dh=dh, dw=dw, workspace=workspace)
     if dh is None and dw is None and workspace is None and grad_dtype in _DTYPES:
-        out = _native().linear_ce_bwd(h, w, target, lse, dloss, dlse, softcap, grad_dtype is _F32, stream)
+        out = _native().linear_ce_bwd(h, w, target, lse, dloss, dlse, softcap, grad_dtype is _F32, None)
         if out.__class__ is dict:
             return out
         if out is not None:
@@ -292,7 +307,7 @@ def linear_ce_bwd(h, w, target, lse, dloss, dlse=None, *, softcap=0.0, grad_dtyp
     _same_device(h, lse=lse, dloss=dloss, dlse=dlse, dh=dh, dw=dw)
     workspace = _ce_workspace(n, d, v, 1, workspace, dev)
     st = lib().lm_linear_ce_bwd(n, d, v, softcap, _p(h), sh, _p(w), _p(target), _p(lse), _p(dloss), _p(dlse), _p(dh),
-                                _p(dw), _code(dh.dtype), _p(workspace), _nbytes(workspace), _stream(stream))
+                                _p(dw), _code(dh.dtype), _p(workspace), _nbytes(workspace), _stream(None))
     _check(st, "lm_linear_ce_bwd")
     return dict(dh=dh, dw=dw)
 
