@@ -147,7 +147,7 @@ struct CeArgs {
 struct CePlan {
     int chunk;   // vocabulary entries a backward pass takes at a time (a multiple of 256)
     int splits;  // ranges of a chunk summed apart for dh
-    int dz, dh, dw;  // tile shapes of the three products
+    int dh;      // tile shape of its product
     int few;     // columns of a transposed dz (32, 64, 128 or 256), 0 with many tokens
 };
 int ce_parts(int n, int d, int v);

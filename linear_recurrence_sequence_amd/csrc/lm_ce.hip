@@ -49,9 +49,10 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
 // P = w (vocabulary), Q = h (tokens): a lane's results are 4 FM logits of each
 // of FN tokens, so a token's maximum and sum are formed in registers, joined
 // over the four lanes that share its column and then, through LDS, over the waves that
-// share its tile.
+// share its tile.  w holds entries [vfirst, vfirst + a.v) here, whose tiles' statistics are
+// parts from `part` on.
 template <class T, bool CAP>
-__global__ __launch_bounds__(T::THREADS) void ce_stats_kernel(const CeArgs a, int np, int nq) {
+__global__ __launch_bounds__(T::THREADS) void ce_stats_kernel(const CeArgs a, int np, int nq, int vfirst, int part) {
     __shared__ __attribute__((aligned(1024))) char lds[T::LDS_BYTES];
     __shared__ int target[T::TILE_Q];
     __shared__ float2 stat[T::WAVES_P][T::TILE_Q];
@@ -59,7 +60,7 @@ __global__ __launch_bounds__(T::THREADS) void ce_stats_kernel(const CeArgs a, in
     int tp, tq;
     tile_of(np, nq, blockIdx.x, &tp, &tq);
     for (int i = threadIdx.x; i < BN; i += T::THREADS) {  // read after the barriers of the product
-        const int64_t y = tq * BN + i < a.n ? a.target[tq * BN + i] : -1;
+        const int64_t y = tq * BN + i < a.n ? a.target[tq * BN + i] - vfirst : -1;
         target[i] = y >= 0 && y < a.v ? (int)y : -1;
     }
     T t;
@@ -87,16 +88,18 @@ __global__ __launch_bounds__(T::THREADS) void ce_stats_kernel(const CeArgs a, in
 #pragma unroll
     for (int j = 0; j < T::FN; ++j) {
         const int col = T::row_q(j) + (lane & 15), y = target[col] - v0;
-        float top = -__builtin_inff(), hit = 0.0f;
-        bool mine = false;
+        float top = -__builtin_inff();
+        if (__ballot(y >= 0 && y < BM)) {  // seldom: a target among this tile's entries
+#pragma unroll
+            for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (y == T::row_p(i) + r) a.picked[tq * BN + col] = t.acc[i][j][r];
+        }
 #pragma unroll
         for (int i = 0; i < T::FM; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float z = t.acc[i][j][r];
-                if (y == T::row_p(i) + r) hit = z, mine = true;
-                top = fmaxf(top, z);
-            }
+            for (int r = 0; r < 4; ++r) top = fmaxf(top, t.acc[i][j][r]);
         top = fmaxf(top, __shfl_xor(top, 16));
         top = LOG2E * fmaxf(top, __shfl_xor(top, 32));
         // an infinite maximum is not subtracted: inf - inf would be NaN where the sum is inf or 0
@@ -108,7 +111,6 @@ __global__ __launch_bounds__(T::THREADS) void ce_stats_kernel(const CeArgs a, in
             for (int r = 0; r < 4; ++r) sum += __builtin_amdgcn_exp2f(fmaf(t.acc[i][j][r], LOG2E, -base));
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
-        if (mine) a.picked[tq * BN + col] = hit;
         if (lane < 16) stat[wave_p][col] = make_float2(top, sum);
     }
     __syncthreads();
@@ -117,7 +119,7 @@ __global__ __launch_bounds__(T::THREADS) void ce_stats_kernel(const CeArgs a, in
         float2 s = stat[0][i];
 #pragma unroll
         for (int k = 1; k < T::WAVES_P; ++k) s = join(s, stat[k][i]);
-        reinterpret_cast<float2*>(a.part)[(int64_t)tp * a.n + tq * BN + i] = s;
+        reinterpret_cast<float2*>(a.part)[(int64_t)(part + tp) * a.n + tq * BN + i] = s;
     }
 }
 
@@ -275,6 +277,7 @@ __global__ __launch_bounds__(T::THREADS) void ce_dz_kernel(const CeArgs a, int n
         const CeToken k = tok < m ? token[T::row_q(j) + (lane & 15)] : CeToken{0.0f, 0.0f, 0.0f, -1};
         const int y = k.target - vfirst - v0;  // no row of this wave where there is no target: rows + v0 + vfirst is not negative
         uint16_t* out = static_cast<uint16_t*>(a.dz) + (int64_t)tok * ld + v0;
+        const bool hit = __ballot(y >= 0 && y < BM) != 0;  // seldom: a target among this tile's entries
 #pragma unroll
         for (int i = 0; i < T::FM; ++i) {
             float g[4];
@@ -287,8 +290,16 @@ __global__ __launch_bounds__(T::THREADS) void ce_dz_kernel(const CeArgs a, int n
                     slope = (1.0f - th) * (1.0f + th);
                 }
                 g[r] = __builtin_amdgcn_exp2f(fmaf(z, LOG2E, -k.base)) * k.c;
-                if (y == T::row_p(i) + r) g[r] -= k.dl;
-                if (CAP) g[r] *= slope;
+                if (CAP) t.acc[i][j][r] = slope;
+            }
+            if (hit) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (y == T::row_p(i) + r) g[r] -= k.dl;
+            }
+            if (CAP) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) g[r] *= t.acc[i][j][r];
             }
             if (a.few) {
                 if (tok >= m) g[0] = g[1] = g[2] = g[3] = 0.0f;
@@ -525,23 +536,43 @@ constexpr int kFew = 256;  // tokens up to which the backward goes by the bytes 
 constexpr int64_t kMostDz = (int64_t)128 << 20;  // elements of dz held at once
 
 // Time of a product of p x q results over k, in microseconds: rounds of
-// workgroups times steps of 64, with three steps' worth of start and end a tile.
-// A round's step takes 1.54 us with large tiles and 1.04 us with small ones (half the
-// flops), both measured over long k with every CU busy.
+// workgroups, each its steps of 64 and the start and end of a tile.  A large tile's step
+// takes 1.45 us and its start and end 6; two small ones of a CU 1.0 and 5, and one
+// alone 0.7 (measured over long and short k with the CUs busy).
 double product_us(Shape s, int64_t p, int64_t q, int64_t k) {
-    const int64_t tiles = ceil_div(p, kBM[s]) * ceil_div(q, kBN[s]), slots = s == LARGE ? 256 : 512;
-    return (double)ceil_div(tiles, slots) * (double)(ceil_div(k, GEMM_BK) + 3) * (s == LARGE ? 1.54 : 1.04);
+    const int64_t tiles = ceil_div(p, kBM[s]) * ceil_div(q, kBN[s]);
+    const double steps = (double)ceil_div(k, GEMM_BK);
+    if (s == LARGE) return (double)ceil_div(tiles, 256) * (steps * 1.45 + 6.0);
+    const int64_t rest = tiles % 512;
+    return (double)(tiles / 512) * (steps + 5.0) + (rest == 0 ? 0.0 : rest <= 256 ? steps * 0.7 + 5.0 : steps + 5.0);
 }
-Shape shape_for(int64_t p, int64_t q, int64_t k) {
-    return product_us(LARGE, p, q, k) <= product_us(SMALL, p, q, k) ? LARGE : SMALL;
+
+// How many of `rows` vocabulary entries go by large tiles, against `other` rows
+// over k: all, none, or the whole rounds of them, the rest then going by small
+// tiles in a launch of its own (486 x 2384 x 33847 is 266 large tiles, ten more than a
+// round).  A multiple of 256, or all.
+int64_t large_rows(int64_t rows, int64_t other, int64_t k, double* us = nullptr) {
+    const int64_t across = ceil_div(other, 256), whole = ceil_div(rows, 256) * across / 256 * 256 / across * 256;
+    int64_t best = 0;
+    double least = product_us(SMALL, rows, other, k);
+    for (int64_t large : {rows, whole}) {
+        if (large <= 0 || large > rows) continue;
+        // two launches have to be worth a tenth
+        const double t = large == rows ? product_us(LARGE, rows, other, k)
+                                       : 1.1 * (product_us(LARGE, large, other, k) + product_us(SMALL, rows - large, other, k) + 3.0);
+        if (t <= least) least = t, best = large;
+    }
+    if (us) *us = least;
+    return best;
 }
 
 }  // namespace
 
-// Tile of the forward product.
-static Shape stats_shape(int n, int d, int v) { return n <= 32 ? FEW : shape_for(v, n, d); }
-
-int ce_parts(int n, int d, int v) { return (int)ceil_div(v, kBM[stats_shape(n, d, v)]); }
+int ce_parts(int n, int d, int v) {
+    if (n <= 32) return (int)ceil_div(v, kBM[FEW]);
+    const int64_t large = large_rows(v, n, d);
+    return (int)(ceil_div(large, 256) + ceil_div(v - large, 128));
+}
 
 // Chunks of the vocabulary, tiles and the ranges that dh is summed over: the
 // cheapest by product_us and the bytes of dh's partial sums, over the chunk
@@ -554,7 +585,6 @@ CePlan ce_plan(int n, int d, int v) {
         const int64_t chunks = ceil_div(v, kMostDz / p.few / 256 * 256);
         p.chunk = (int)(ceil_div(ceil_div(v, chunks), 256) * 256);
         p.dh = n <= 32 ? FEW : SMALL;
-        p.dz = n <= 32 ? FEW : shape_for(std::min(p.chunk, v), n, d);
         // the product over the vocabulary reads w once: enough ranges to fill the chip, four steps or more each
         const int64_t tiles = ceil_div(d, kBM[p.dh]) * ceil_div(n, kBN[p.dh]), want = (p.dh == FEW ? 1024 : 512) / tiles;
         p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(want, std::min(p.chunk, v) / (4 * GEMM_BK)));
@@ -567,13 +597,14 @@ CePlan ce_plan(int n, int d, int v) {
         const int64_t chunk = ceil_div(ceil_div(v, chunks), 256) * 256, count = std::min<int64_t>(chunk, v);
         CePlan p{};
         p.chunk = (int)chunk;
-        p.dz = shape_for(count, n, d);
-        p.dw = shape_for(d, count, n);
-        double us = product_us((Shape)p.dz, count, n, d) + product_us((Shape)p.dw, d, count, n), dh_us = 0.0;
+        double us, dw_us, dh_us = 0.0;
+        large_rows(count, n, d, &us);
+        large_rows(count, d, n, &dw_us);
+        us += dw_us;
         for (int s = LARGE; s <= SMALL; ++s) {
             for (int splits = 1; splits <= 64 && (splits == 1 || count / splits >= 8 * GEMM_BK); ++splits) {
                 // the partial sums are written, and read by the next chunk or the last launch
-                const double t = product_us((Shape)s, d, (int64_t)n * splits, ceil_div(count, splits)) + (double)splits * n * d * 8 / 4.5e6;
+                const double t = product_us((Shape)s, d, ceil_div(n, kBN[s]) * kBN[s] * splits, ceil_div(count, splits)) + (double)splits * n * d * 8 / 4.5e6;
                 if (dh_us == 0.0 || t < dh_us) dh_us = t, p.dh = s, p.splits = splits;
             }
         }
@@ -595,12 +626,21 @@ CePlan ce_plan(int n, int d, int v) {
 #define CE_DZ_CAP(...) ce_dz_kernel<__VA_ARGS__, true>
 
 hipError_t launch_ce_fwd(const CeArgs& a, hipStream_t s) {
-    const Shape sh = stats_shape(a.n, a.d, a.v);
-    const int np = (int)ceil_div(a.v, kBM[sh]), nq = (int)ceil_div(a.n, kBN[sh]);
-    const dim3 g((unsigned)(np * nq));
-    if (a.cap > 0.0f) CE_SHAPES(sh, K_LM_CE_STATS, g, CE_STATS_CAP, Wide, false, false, a, np, nq);
-    else CE_SHAPES(sh, K_LM_CE_STATS, g, CE_STATS, Wide, false, false, a, np, nq);
-    LRS_LAUNCH(K_LM_CE_JOIN, ce_join_kernel, dim3((unsigned)ceil_div(a.n, 16)), dim3(1024), 0, s, a, np);
+    const int large = a.n <= 32 ? 0 : (int)large_rows(a.v, a.n, a.d);
+    int part = 0;
+    for (int v0 = 0; v0 < a.v;) {
+        const int sh = a.n <= 32 ? FEW : v0 < large ? LARGE : SMALL;
+        CeArgs p = a;
+        p.w = static_cast<const char*>(a.w) + (int64_t)v0 * a.d * 2;
+        p.v = (sh == LARGE ? large : a.v) - v0;
+        const int np = (int)ceil_div(p.v, kBM[sh]), nq = (int)ceil_div(a.n, kBN[sh]);
+        const dim3 g((unsigned)(np * nq));
+        if (a.cap > 0.0f) CE_SHAPES(sh, K_LM_CE_STATS, g, CE_STATS_CAP, Wide, false, false, p, np, nq, v0, part);
+        else CE_SHAPES(sh, K_LM_CE_STATS, g, CE_STATS, Wide, false, false, p, np, nq, v0, part);
+        part += np;
+        v0 += p.v;
+    }
+    LRS_LAUNCH(K_LM_CE_JOIN, ce_join_kernel, dim3((unsigned)ceil_div(a.n, 16)), dim3(1024), 0, s, a, part);
     return hipGetLastError();
 }
 
@@ -623,11 +663,19 @@ hipError_t launch_ce_bwd(const CeArgs& args, hipStream_t s) {
     int used = 1;  // ranges of the first chunk, which is the longest
     for (int v0 = 0; v0 < a.v; v0 += pl.chunk) {
         const int count = std::min(pl.chunk, a.v - v0), ld = pl.chunk;
-        {
-            const int np = (int)ceil_div(count, kBM[pl.dz]);
-            const dim3 g((unsigned)(np * ceil_div(pl.few ? pl.few : a.n, kBN[pl.dz])));
-            if (a.cap > 0.0f) CE_SHAPES(pl.dz, K_LM_CE_DZ, g, CE_DZ_CAP, Wide, false, false, a, np, v0, count, ld);
-            else CE_SHAPES(pl.dz, K_LM_CE_DZ, g, CE_DZ, Wide, false, false, a, np, v0, count, ld);
+        const auto part_of = [&](int at) {  // the arguments with dz from entry `at` of the chunk on
+            CeArgs p = a;
+            p.dz = static_cast<uint16_t*>(a.dz) + (int64_t)at * (a.few ? a.few : 1);
+            return p;
+        };
+        for (int at = 0, large = a.n <= 32 ? 0 : (int)large_rows(count, a.n, a.d); at < count;) {
+            const int sh = a.n <= 32 ? FEW : at < large ? LARGE : SMALL, some = (sh == LARGE ? large : count) - at;
+            const CeArgs p = part_of(at);
+            const int np = (int)ceil_div(some, kBM[sh]);
+            const dim3 g((unsigned)(np * ceil_div(pl.few ? pl.few : a.n, kBN[sh])));
+            if (a.cap > 0.0f) CE_SHAPES(sh, K_LM_CE_DZ, g, CE_DZ_CAP, Wide, false, false, p, np, v0 + at, some, ld);
+            else CE_SHAPES(sh, K_LM_CE_DZ, g, CE_DZ, Wide, false, false, p, np, v0 + at, some, ld);
+            at += some;
         }
         {
             const int np = (int)ceil_div(a.d, kBM[pl.dh]);
@@ -647,10 +695,15 @@ hipError_t launch_ce_bwd(const CeArgs& args, hipStream_t s) {
             else if (pl.few == 128) LRS_LAUNCH(K_LM_CE_DW, ce_dw_few_kernel<4>, g, dim3(256), 0, s, a, v0, count);
             else LRS_LAUNCH(K_LM_CE_DW, ce_dw_few_kernel<8>, g, dim3(256), 0, s, a, v0, count);
         } else {
-            const int np = (int)ceil_div(a.d, kBM[pl.dw]), nq = (int)ceil_div(count, kBN[pl.dw]);
-            const dim3 g((unsigned)(np * nq));
-            if (pl.dw == LARGE) LRS_LAUNCH(K_LM_CE_DW, (ce_dw_kernel<Large<true, true>>), g, dim3(Large<true, true>::THREADS), 0, s, a, np, nq, v0, count, ld);
-            else LRS_LAUNCH(K_LM_CE_DW, (ce_dw_kernel<Small<true, true>>), g, dim3(Small<true, true>::THREADS), 0, s, a, np, nq, v0, count, ld);
+            for (int at = 0, large = (int)large_rows(count, a.d, a.n); at < count;) {
+                const int sh = at < large ? LARGE : SMALL, some = (sh == LARGE ? large : count) - at;
+                const CeArgs p = part_of(at);
+                const int np = (int)ceil_div(a.d, kBM[sh]), nq = (int)ceil_div(some, kBN[sh]);
+                const dim3 g((unsigned)(np * nq));
+                if (sh == LARGE) LRS_LAUNCH(K_LM_CE_DW, (ce_dw_kernel<Large<true, true>>), g, dim3(Large<true, true>::THREADS), 0, s, p, np, nq, v0 + at, some, ld);
+                else LRS_LAUNCH(K_LM_CE_DW, (ce_dw_kernel<Small<true, true>>), g, dim3(Small<true, true>::THREADS), 0, s, p, np, nq, v0 + at, some, ld);
+                at += some;
+            }
         }
     }
     const int64_t quads = (int64_t)a.n * a.d / 4;
