@@ -17,7 +17,7 @@
 // every output come from there.  A row belongs to W waves of a workgroup, each
 // lane holding NV groups of 4 consecutive elements, 256 W elements apart, so
 // every load of a wave covers whole lines.  With W = 1 a workgroup holds four
-// rows and needs no barrier.  Workgroups walk over rows with the weights in
+// rows (eight or 16 of up to 128 or 64 columns, on half or a quarter of a wave) and needs no barrier.  Workgroups walk over rows with the weights in
 // registers, and the backward keeps its column sums there until the end.
 // 32768 x 2560, FP32 stream and BF16 branch with a gate: forward 221 us, 5.3 TB/s;
 // backward 322 us, 5.7 TB/s (a large copy runs at 4.7 TB/s).
@@ -28,13 +28,18 @@ namespace {
 
 constexpr int MAX_WAVES = 16;
 
-// Sum over the row's waves.  `slot` alternates between calls, so one barrier
+// Sum over the row's lanes: L, or (L = 0) the workgroup's.  `slot` alternates between calls, so one barrier
 // a reduction is enough: a slot is written again only after the barrier of the
 // reduction in between.
-template <bool ONE>
+template <int L>
 __device__ __forceinline__ float row_sum(float v, float (*slots)[MAX_WAVES], int slot, int waves) {
+    if (L > 0 && L < 64) {
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor(v, o);
+        return v;
+    }
     v = wave_sum(v);
-    if (ONE) return v;
+    if (L > 0) return v;
     if ((threadIdx.x & 63) == 0) slots[slot][threadIdx.x >> 6] = v;
     __syncthreads();
     float s = 0.0f;
@@ -46,12 +51,32 @@ __device__ __forceinline__ float sigmoid(float g) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g));
 }
 
-// Which elements a lane holds: group c starts at column c * 4 T + 4 t.
+// Which elements a lane holds: group c starts at column c * 4 T + 4 t.  Where
+// the width is no multiple of 4 (TAIL) the group that the row ends in is loaded as the
+// row's last four elements and put in place by take(), so that no load stands in a
+// branch of its own (each would be waited for there).
 template <class T, bool TAIL>
 __device__ __forceinline__ Quad<T> row_load(const T* row, int col, int d) {
+    if (TAIL) {
+        if (d < 4) return col < d ? Quad<T>::load_some(row, d) : Quad<T>::zero();
+        return Quad<T>::load(row + (col + 4 <= d ? col : d - 4));
+    }
     if (col + 4 <= d) return Quad<T>::load(row + col);
-    if (TAIL && col < d) return Quad<T>::load_some(row + col, d - col);
     return Quad<T>::zero();
+}
+template <bool TAIL, class T>
+__device__ __forceinline__ void take(const Quad<T>& q, int col, int d, float* f) {
+    q.get(f);
+    if (TAIL) {
+        const int n = d < 4 && col < d ? 4 : d - col;  // this lane's elements, 4 or more: all
+        if (n < 4) {
+            const float a = f[1], b = f[2], c = f[3];
+            f[0] = n == 3 ? a : n == 2 ? b : n == 1 ? c : 0.0f;
+            f[1] = n == 3 ? b : n == 2 ? c : 0.0f;
+            f[2] = n == 3 ? c : 0.0f;
+            f[3] = 0.0f;
+        }
+    }
 }
 template <class T, bool TAIL>
 __device__ __forceinline__ void row_store(T* row, int col, int d, const float* f) {
@@ -61,19 +86,19 @@ __device__ __forceinline__ void row_store(T* row, int col, int d, const float* f
 template <bool TAIL>
 __device__ __forceinline__ void weight_load(const float* w, int col, int d, float missing, float* f) {
     if (w) {
-        row_load<float, TAIL>(w, col, d).get(f);
+        take<TAIL>(row_load<float, TAIL>(w, col, d), col, d, f);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[i] = missing;
     }
 }
 
-// TAIL: d is not a multiple of 4.  ONE: a row is one wave's.
-template <class ST, class BR, int NV, bool ONE, bool TAIL>
-__global__ __launch_bounds__(ONE ? 256 : 1024) void norm_fwd_kernel(const NormArgs a) {
+// TAIL: d is not a multiple of 4.  L: lanes of a row, 0: all of the workgroup's.
+template <class ST, class BR, int NV, int L, bool TAIL>
+__global__ __launch_bounds__(L > 0 ? 256 : 1024) void norm_fwd_kernel(const NormArgs a) {
     __shared__ float slots[2][MAX_WAVES];
-    const int T = ONE ? 64 : blockDim.x, t = ONE ? threadIdx.x & 63 : threadIdx.x, waves = T >> 6;
-    const int per = ONE ? 4 : 1, mine = ONE ? threadIdx.x >> 6 : 0;
+    const int T = L > 0 ? L : blockDim.x, t = L > 0 ? threadIdx.x % L : threadIdx.x, waves = T >> 6;
+    const int per = L > 0 ? 256 / L : 1, mine = L > 0 ? threadIdx.x / L : 0;
     const bool full = a.w_post != nullptr, gated = a.gate != nullptr, silu = a.gate_act == 2;
     const float inv_d = 1.0f / (float)a.d;
     float w1[NV][4], w2[NV][4];
@@ -89,7 +114,7 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void norm_fwd_kernel(const NormAr
     }
     for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < a.rows; row0 += (int64_t)gridDim.x * per) {
         const int64_t row = row0 + mine;
-        if (ONE && row >= a.rows) break;  // no barrier in this form
+        if (L > 0 && row >= a.rows) break;  // no barrier in this form
         Quad<ST> qx[NV];
         Quad<BR> qy[NV], qg[NV];
         const ST* x = static_cast<const ST*>(a.x) + row * a.x_stride;
@@ -108,35 +133,35 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void norm_fwd_kernel(const NormAr
 #pragma unroll
             for (int c = 0; c < NV; ++c) {
                 float f[4];
-                qy[c].get(f);
+                take<TAIL>(qy[c], c * 4 * T + 4 * t, a.d, f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s = fmaf(f[i], f[i], s);
             }
-            rs1 = 1.0f / sqrtf(row_sum<ONE>(s, slots, 0, waves) * inv_d + a.eps);
+            rs1 = 1.0f / sqrtf(row_sum<L>(s, slots, 0, waves) * inv_d + a.eps);
         }
         float r[NV][4], s = 0.0f;
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             float f[4], u[4];
-            qy[c].get(u);
+            take<TAIL>(qy[c], c * 4 * T + 4 * t, a.d, u);
 #pragma unroll
             for (int i = 0; i < 4; ++i) u[i] = u[i] * rs1 * w1[c][i];
             if (gated) {
-                qg[c].get(f);
+                take<TAIL>(qg[c], c * 4 * T + 4 * t, a.d, f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float sg = sigmoid(f[i]);
                     u[i] *= silu ? sg * f[i] : sg;
                 }
             }
-            qx[c].get(f);
+            take<TAIL>(qx[c], c * 4 * T + 4 * t, a.d, f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 r[c][i] = f[i] + u[i];
                 s = fmaf(r[c][i], r[c][i], s);
             }
         }
-        const float rs2 = 1.0f / sqrtf(row_sum<ONE>(s, slots, 1, waves) * inv_d + a.eps);
+        const float rs2 = 1.0f / sqrtf(row_sum<L>(s, slots, 1, waves) * inv_d + a.eps);
         ST* ro = static_cast<ST*>(a.r) + row * a.d;
         BR* no = static_cast<BR*>(a.n) + row * a.d;
 #pragma unroll
@@ -152,15 +177,15 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void norm_fwd_kernel(const NormAr
             a.stats[2 * row + 1] = rs2;
         }
         // the plain form has one reduction a row: keep its slot from being written while others still read it
-        if (!ONE && !full) __syncthreads();
+        if (L == 0 && !full) __syncthreads();
     }
 }
 
-template <class ST, class BR, int NV, bool ONE, bool TAIL>
-__global__ __launch_bounds__(ONE ? 256 : 1024) void norm_bwd_kernel(const NormArgs a) {
+template <class ST, class BR, int NV, int L, bool TAIL>
+__global__ __launch_bounds__(L > 0 ? 256 : 1024) void norm_bwd_kernel(const NormArgs a) {
     __shared__ float slots[2][MAX_WAVES];
-    const int T = ONE ? 64 : blockDim.x, t = ONE ? threadIdx.x & 63 : threadIdx.x, waves = T >> 6;
-    const int per = ONE ? 4 : 1, mine = ONE ? threadIdx.x >> 6 : 0;
+    const int T = L > 0 ? L : blockDim.x, t = L > 0 ? threadIdx.x % L : threadIdx.x, waves = T >> 6;
+    const int per = L > 0 ? 256 / L : 1, mine = L > 0 ? threadIdx.x / L : 0;
     const bool full = a.w_post != nullptr, gated = a.gate != nullptr, silu = a.gate_act == 2;
     const float inv_d = 1.0f / (float)a.d;
     float w1[NV][4], w2[NV][4], sum2[NV][4], sums[NV][4];
@@ -179,7 +204,7 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void norm_bwd_kernel(const NormAr
     }
     for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < a.rows; row0 += (int64_t)gridDim.x * per) {
         const int64_t row = row0 + mine;
-        if (ONE && row >= a.rows) break;
+        if (L > 0 && row >= a.rows) break;
         Quad<ST> qx[NV], qr[NV];
         Quad<BR> qy[NV], qg[NV], qn[NV];
         const ST* x = static_cast<const ST*>(a.x) + row * a.x_stride;
@@ -203,21 +228,21 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void norm_bwd_kernel(const NormAr
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             float u[4], f[4];
-            qy[c].get(u);
+            take<TAIL>(qy[c], c * 4 * T + 4 * t, a.d, u);
 #pragma unroll
             for (int i = 0; i < 4; ++i) u[i] = u[i] * rs1 * w1[c][i];
             if (gated) {
-                qg[c].get(f);
+                take<TAIL>(qg[c], c * 4 * T + 4 * t, a.d, f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float sg = sigmoid(f[i]);
                     u[i] *= silu ? sg * f[i] : sg;
                 }
             }
-            qx[c].get(f);
+            take<TAIL>(qx[c], c * 4 * T + 4 * t, a.d, f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) rh[c][i] = (f[i] + u[i]) * rs2;
-            qn[c].get(f);
+            take<TAIL>(qn[c], c * 4 * T + 4 * t, a.d, f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float p = f[i] * rh[c][i];
@@ -225,7 +250,7 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void norm_bwd_kernel(const NormAr
                 s = fmaf(p, w2[c][i], s);
             }
         }
-        const float m2 = row_sum<ONE>(s, slots, 0, waves) * inv_d;
+        const float m2 = row_sum<L>(s, slots, 0, waves) * inv_d;
         // v, dx, dgate, the column sum S, and q yh for the second mean
         ST* dx = static_cast<ST*>(a.dx) + row * a.d;
         BR* dy = static_cast<BR*>(a.dy) + row * a.d;
@@ -235,16 +260,16 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void norm_bwd_kernel(const NormAr
         for (int c = 0; c < NV; ++c) {
             const int col = c * 4 * T + 4 * t;
             float v[4], f[4], yh[4], da[4];
-            qr[c].get(v);
-            qn[c].get(f);
+            take<TAIL>(qr[c], c * 4 * T + 4 * t, a.d, v);
+            take<TAIL>(qn[c], c * 4 * T + 4 * t, a.d, f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] += rs2 * (f[i] * w2[c][i] - rh[c][i] * m2);
             row_store<ST, TAIL>(dx, col, a.d, v);
-            qy[c].get(yh);
+            take<TAIL>(qy[c], c * 4 * T + 4 * t, a.d, yh);
 #pragma unroll
             for (int i = 0; i < 4; ++i) yh[i] *= rs1;
             if (gated) {
-                qg[c].get(f);
+                take<TAIL>(qg[c], c * 4 * T + 4 * t, a.d, f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float sg = sigmoid(f[i]), slope = sg * (1.0f - sg);
@@ -260,34 +285,39 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void norm_bwd_kernel(const NormAr
                 s = fmaf(rh[c][i], yh[i], s);
             }
         }
-        const float m1 = full ? row_sum<ONE>(s, slots, 1, waves) * inv_d : 0.0f;
+        const float m1 = full ? row_sum<L>(s, slots, 1, waves) * inv_d : 0.0f;
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             const int col = c * 4 * T + 4 * t;
             float yh[4];
-            qy[c].get(yh);
+            take<TAIL>(qy[c], c * 4 * T + 4 * t, a.d, yh);
             if (full) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) rh[c][i] = rs1 * (rh[c][i] - yh[i] * rs1 * m1);
             }
             row_store<BR, TAIL>(dy, col, a.d, rh[c]);
         }
-        if (!ONE && !full) __syncthreads();
+        if (L == 0 && !full) __syncthreads();
     }
     // column sums of this workgroup's rows (in a fixed order over its waves)
     float* part = a.part + (int64_t)blockIdx.x * 2 * a.d;
-    if (ONE) {
-        __shared__ float buf[4][NV * 256];
+    if (L > 0) {
+        constexpr int ROWS = L > 0 ? 256 / L : 1, LINE = NV * 4 * (L > 0 ? L : 1);
+        __shared__ float buf[ROWS][LINE];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             if (k) __syncthreads();
 #pragma unroll
             for (int c = 0; c < NV; ++c)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) buf[mine][c * 256 + 4 * t + i] = k ? sums[c][i] : sum2[c][i];
+                for (int i = 0; i < 4; ++i) buf[mine][c * 4 * L + 4 * t + i] = k ? sums[c][i] : sum2[c][i];
             __syncthreads();
-            for (int col = threadIdx.x; col < a.d; col += 256)
-                part[k * a.d + col] = (buf[0][col] + buf[1][col]) + (buf[2][col] + buf[3][col]);
+            for (int col = threadIdx.x; col < a.d; col += 256) {
+                float s = 0.0f;
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) s += buf[r][col];
+                part[k * a.d + col] = s;
+            }
         }
     } else {
 #pragma unroll
@@ -342,42 +372,46 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* part, in
 // chain of loads and sums).  Of many rows, those up to 1024 columns are one
 // wave's: four rows are then in flight in a workgroup and no barrier stands
 // between them (backward of 4096 x 1024 bf16: 23 us, 31 us with two waves a row;
-// of 32768 x 1024: 103 us, 112 us).  Wider ones take two groups a wave, four above 8192
+// of 32768 x 1024: 103 us, 112 us), up to 128 and 64 columns half a wave's or a
+// quarter's (backward of 32768 x 64 bf16: 15 us, 44 us with a wave a row).  Wider ones take two groups a wave, four above 8192
 // columns, where a row would not fit the 16 waves of a workgroup.
 struct Plan {
-    int nv, waves;
+    int nv, waves, lanes;  // lanes of a row where it is no more than a wave's, else 0
 };
 Plan plan(int64_t rows, int d) {
     const int groups = (int)ceil_div(d, 256);
-    if (rows <= 512 && groups <= MAX_WAVES) return {1, groups};
-    if (groups > 2 && groups <= 4) return {4, 1};
-    if (groups <= 2 * MAX_WAVES) return {2, (int)ceil_div(groups, 2)};
-    return {4, (int)ceil_div(groups, 4)};
+    if (groups == 1) return {1, 1, d <= 64 ? 16 : d <= 128 ? 32 : 64};
+    if (rows <= 512 && groups <= MAX_WAVES) return {1, groups, 0};
+    if (groups > 2 && groups <= 4) return {4, 1, 64};
+    if (groups <= 2 * MAX_WAVES) return {2, (int)ceil_div(groups, 2), groups <= 2 ? 64 : 0};
+    return {4, (int)ceil_div(groups, 4), 0};
 }
 
-template <bool BWD, class ST, class BR, int NV, bool ONE>
+template <bool BWD, class ST, class BR, int NV, int L>
 void launch_one(const NormArgs& a, dim3 g, dim3 b, hipStream_t s) {
     if (a.d % 4 == 0) {
-        if (BWD) LRS_LAUNCH(K_LM_NORM_BWD, (norm_bwd_kernel<ST, BR, NV, ONE, false>), g, b, 0, s, a);
-        else LRS_LAUNCH(K_LM_NORM, (norm_fwd_kernel<ST, BR, NV, ONE, false>), g, b, 0, s, a);
+        if (BWD) LRS_LAUNCH(K_LM_NORM_BWD, (norm_bwd_kernel<ST, BR, NV, L, false>), g, b, 0, s, a);
+        else LRS_LAUNCH(K_LM_NORM, (norm_fwd_kernel<ST, BR, NV, L, false>), g, b, 0, s, a);
     } else {
-        if (BWD) LRS_LAUNCH(K_LM_NORM_BWD, (norm_bwd_kernel<ST, BR, NV, ONE, true>), g, b, 0, s, a);
-        else LRS_LAUNCH(K_LM_NORM, (norm_fwd_kernel<ST, BR, NV, ONE, true>), g, b, 0, s, a);
+        if (BWD) LRS_LAUNCH(K_LM_NORM_BWD, (norm_bwd_kernel<ST, BR, NV, L, true>), g, b, 0, s, a);
+        else LRS_LAUNCH(K_LM_NORM, (norm_fwd_kernel<ST, BR, NV, L, true>), g, b, 0, s, a);
     }
 }
 
 template <bool BWD, class ST, class BR>
 void launch_typed(const NormArgs& a, int blocks, hipStream_t s) {
     const Plan p = plan(a.rows, a.d);
-    const dim3 g(blocks), b(p.waves == 1 ? 256 : 64 * p.waves);
-    if (p.waves == 1) {
-        if (p.nv == 1) launch_one<BWD, ST, BR, 1, true>(a, g, b, s);
-        else if (p.nv == 2) launch_one<BWD, ST, BR, 2, true>(a, g, b, s);
-        else launch_one<BWD, ST, BR, 4, true>(a, g, b, s);
+    const dim3 g(blocks), b(p.lanes ? 256 : 64 * p.waves);
+    if (p.lanes) {
+        if (p.lanes == 16) launch_one<BWD, ST, BR, 1, 16>(a, g, b, s);
+        else if (p.lanes == 32) launch_one<BWD, ST, BR, 1, 32>(a, g, b, s);
+        else if (p.nv == 1) launch_one<BWD, ST, BR, 1, 64>(a, g, b, s);
+        else if (p.nv == 2) launch_one<BWD, ST, BR, 2, 64>(a, g, b, s);
+        else launch_one<BWD, ST, BR, 4, 64>(a, g, b, s);
     } else {
-        if (p.nv == 1) launch_one<BWD, ST, BR, 1, false>(a, g, b, s);
-        else if (p.nv == 2) launch_one<BWD, ST, BR, 2, false>(a, g, b, s);
-        else launch_one<BWD, ST, BR, 4, false>(a, g, b, s);
+        if (p.nv == 1) launch_one<BWD, ST, BR, 1, 0>(a, g, b, s);
+        else if (p.nv == 2) launch_one<BWD, ST, BR, 2, 0>(a, g, b, s);
+        else launch_one<BWD, ST, BR, 4, 0>(a, g, b, s);
     }
 }
 
@@ -397,17 +431,20 @@ void launch_any(const NormArgs& a, int stream_f32, int branch_f32, int blocks, h
 // Workgroups that walk over the rows.  Each writes its column sums, and HBM
 // serves few long streams better than many: with 5 waves a row (32768 x 2560)
 // 512 workgroups take 322 us, 256 478, 768 380, 1024 410; with 16 (4096 x 8192)
-// 256 take 153 us, 512 165; with 2 (8192 x 1024) 1024 took 47 us, 512 55.
+// 256 take 153 us, 512 165; with 2 (8192 x 1024) 1024 took 47 us, 512 55; narrow rows
+// that are less than a wave's work wait for memory more (32768 x 256: 1024 take 35 us, 512 41).
 int lm_norm_bwd_blocks(int64_t rows, int d) {
-    const int waves = plan(rows, d).waves, per = waves == 1 ? 4 : 1;
-    return (int)std::min<int64_t>(ceil_div(rows, per), waves > 8 ? 256 : waves >= 4 || waves == 1 ? 512 : 1024);
+    const Plan p = plan(rows, d);
+    const int most = p.lanes ? (d > 64 && d <= 256 ? 1024 : 512) : p.waves > 8 ? 256 : p.waves >= 4 ? 512 : 1024;
+    return (int)std::min<int64_t>(ceil_div(rows, p.lanes ? 256 / p.lanes : 1), most);
 }
 
 // The forward keeps nothing between rows; only the widest rows gain from
 // fewer workgroups (4096 x 8192: 768 take 87 us, 4096 100; 32768 x 2560: 221 us either way).
 hipError_t launch_norm_fwd(const NormArgs& a, int stream_f32, int branch_f32, hipStream_t s) {
-    const int waves = plan(a.rows, a.d).waves, per = waves == 1 ? 4 : 1;
-    launch_any<false>(a, stream_f32, branch_f32, (int)std::min<int64_t>(ceil_div(a.rows, per), waves > 8 ? 768 : 4096), s);
+    const Plan p = plan(a.rows, a.d);
+    launch_any<false>(a, stream_f32, branch_f32,
+                      (int)std::min<int64_t>(ceil_div(a.rows, p.lanes ? 256 / p.lanes : 1), p.waves > 8 ? 768 : 4096), s);
     return hipGetLastError();
 }
 

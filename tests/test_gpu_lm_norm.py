@@ -245,3 +245,48 @@ def test_a_wave_a_row(rows, d, st, br):
     act = ("silu", "sigmoid", "none")[rows % 3]
     a = make(rows, d, st, br, act, d % 2 == 0, rows + d)
     check(a, act, both(a, act), plain(a, act))
+
+
+def term_sizes(a, act, eps=EPS):
+    """What FP32's roundings are to be measured by over few columns, where results cancel, in 64 bits.  r = x + u may be
+    far smaller than x and u, and norm(r) divides by it: everything behind it carries r's rounding k = (|x| + |u|) rs2 times.
+    A norm's gradient is a difference that over one column cancels but for eps's part.  So: the largest of the terms of
+    n, dx, dy and dgate, times k, and the sums of the magnitudes of the weights' gradients, times k."""
+    t = {k: None if v is None else v.cpu().double() for k, v in a.items()}
+    y, one = t["y"], torch.ones((), dtype=torch.float64)
+    w1, sc = (one, one) if t["w_post"] is None else (t["w_post"], t["scale"])
+    rs1 = one if t["w_post"] is None else 1 / torch.sqrt((y * y).mean(-1, keepdim=True) + eps)
+    g = torch.sigmoid(t["gate"]) if t["gate"] is not None else one
+    f, df = (g, one * 0) if t["gate"] is None else (g * t["gate"], g * (1 + t["gate"] * (1 - g))) if act == "silu" else (g, g * (1 - g))
+    yh = y * rs1
+    u = sc * f * yh * w1
+    r = t["x"] + u
+    rs2 = 1 / torch.sqrt((r * r).mean(-1, keepdim=True) + eps)
+    k = ((t["x"].abs() + u.abs()) * rs2).amax(-1, keepdim=True).clamp_min(1.0)
+    p = (t["dn"] * t["w_pre"]).abs()
+    rh = (r * rs2).abs()
+    v = (t["dr"].abs() + rs2 * (p + rh * (p * rh).mean(-1, keepdim=True))) * k
+    q = v * (sc * f * w1).abs()
+    dy = q if t["w_post"] is None else rs1 * (q + yh.abs() * (q * yh.abs()).mean(-1, keepdim=True))
+    out = dict(n=k * (t["w_pre"].abs() + 0 * rh), dx=v, dy=dy, dgate=v * (sc * yh * w1 * df).abs())
+    out = {key: float(x.max()) for key, x in out.items()}
+    out["dw_pre"] = float((t["dn"].abs() * rh * k).sum(0).max())
+    s = (v * (f * yh).abs()).sum(0)
+    out.update(dw_post=float((s * sc).abs().max()), dscale=float((s * w1).abs().max()))
+    return out
+
+
+@pytest.mark.parametrize("d", [1, 2, 3, 4, 5, 15, 63, 64, 65, 67, 127, 128, 129, 255, 257])
+@pytest.mark.parametrize("rows", [1, 17, 600, 9000])
+def test_narrow_rows(rows, d):
+    """Several rows to a wave, and every remainder of the width by four."""
+    say(f"[norm] narrow rows {rows}x{d}")
+    act = ("silu", "sigmoid", "none")[(rows + d) % 3]
+    st, br = (bf, f32) if d % 2 else (f32, bf)
+    a = make(rows, d, st, br, act, d % 3 != 0, rows + d)
+    (r, n, grads), (rr, rn, rg), size = both(a, act), plain(a, act), term_sizes(a, act)
+    close(r, rr, tag(r, "r"))
+    close(n, rn, tag(n, "n"), size["n"])
+    assert set(grads) == set(rg)
+    for k in rg:
+        close(grads[k], rg[k], tag(grads[k], k), size[k])
