@@ -35,8 +35,26 @@ __device__ __forceinline__ void tile_of(int np, int nq, int b, int* p, int* q) {
     *p = in / size;
 }
 
-__device__ __forceinline__ float cap_tanh(float z, float inv_cap) {  // tanh(z / cap)
-    return 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(2.0f * LOG2E * inv_cap * z));
+// tanh(z / cap) of four logits, in place.  Up to |x| = 1 the continued fraction
+// x / (1 + x^2 / (3 + x^2 / (5 + ...))) to its sixth denominator, off by less than FP32's own
+// rounding there; beyond, which a wave seldom meets, 1 - 2 / (1 + e^2x), which near zero would
+// keep the rounding of 1.
+__device__ __forceinline__ void cap_tanh(f32acc_t& z, float inv_cap) {
+    float top = 0.0f;
+    f32acc_t x, y;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        x[r] = z[r] * inv_cap;
+        y[r] = x[r] * x[r];
+        top = fmaxf(top, y[r]);
+        z[r] = x[r] * fmaf(fmaf(21.0f, y[r], 1260.0f), y[r], 10395.0f) *
+               __builtin_amdgcn_rcpf(fmaf(fmaf(y[r] + 210.0f, y[r], 4725.0f), y[r], 10395.0f));
+    }
+    if (__ballot(top >= 1.0f)) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (!(y[r] < 1.0f)) z[r] = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(2.0f * LOG2E * x[r]));
+    }
 }
 
 // Two (maximum, sum of 2^(z - maximum)) of base-2 logits as one.
@@ -73,8 +91,10 @@ __global__ __launch_bounds__(T::THREADS) void ce_stats_kernel(const CeArgs a, in
         for (int j = 0; j < T::FN; ++j)
 #pragma unroll
             for (int i = 0; i < T::FM; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) t.acc[i][j][r] = a.cap * cap_tanh(t.acc[i][j][r], inv_cap);
+            {
+                cap_tanh(t.acc[i][j], inv_cap);
+                t.acc[i][j] *= a.cap;
+            }
     }
     if ((tp + 1) * BM > a.v) {
 #pragma unroll
@@ -147,11 +167,12 @@ __global__ __launch_bounds__(1024) void ce_join_kernel(const CeArgs a, int parts
     }
     if (l == 0 && tok < a.n) {
         const float base = fabsf(s.x) == __builtin_inff() ? 0.0f : s.x;
-        const float lse = LN2 * (base + __builtin_amdgcn_logf(s.y));
+        const float more = __builtin_amdgcn_logf(s.y);
         const int64_t y = a.target[tok];
-        a.lse[tok] = lse;
-        // a target beyond the vocabulary has no loss: NaN says so
-        a.loss[tok] = y < 0 ? 0.0f : y < a.v ? lse - a.picked[tok] : __builtin_nanf("");
+        a.lse[tok] = LN2 * (base + more);
+        // The loss from differences in base 2, not from the rounded lse: it may be far smaller.
+        // A target beyond the vocabulary has no loss: NaN says so.
+        a.loss[tok] = y < 0 ? 0.0f : y < a.v ? LN2 * (fmaf(-a.picked[tok], LOG2E, base) + more) : __builtin_nanf("");
     }
 }
 
@@ -281,17 +302,10 @@ __global__ __launch_bounds__(T::THREADS) void ce_dz_kernel(const CeArgs a, int n
 #pragma unroll
         for (int i = 0; i < T::FM; ++i) {
             float g[4];
+            if (CAP) cap_tanh(t.acc[i][j], inv_cap);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                float z = t.acc[i][j][r], slope = 1.0f;
-                if (CAP) {
-                    const float th = cap_tanh(z, inv_cap);
-                    z = a.cap * th;
-                    slope = (1.0f - th) * (1.0f + th);
-                }
-                g[r] = __builtin_amdgcn_exp2f(fmaf(z, LOG2E, -k.base)) * k.c;
-                if (CAP) t.acc[i][j][r] = slope;
-            }
+            for (int r = 0; r < 4; ++r)
+                g[r] = __builtin_amdgcn_exp2f(fmaf(t.acc[i][j][r], CAP ? a.cap * LOG2E : LOG2E, -k.base)) * k.c;
             if (hit) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
@@ -299,7 +313,7 @@ __global__ __launch_bounds__(T::THREADS) void ce_dz_kernel(const CeArgs a, int n
             }
             if (CAP) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) g[r] *= t.acc[i][j][r];
+                for (int r = 0; r < 4; ++r) g[r] *= (1.0f - t.acc[i][j][r]) * (1.0f + t.acc[i][j][r]);
             }
             if (a.few) {
                 if (tok >= m) g[0] = g[1] = g[2] = g[3] = 0.0f;
