@@ -8,12 +8,32 @@
 //
 // A workgroup owns a BM x BN tile of C and walks over k in steps of 64.  Both
 // operands' tiles go from memory straight into LDS (16 bytes a lane, no
-// registers in between), into one of two buffers while the other one is
-// multiplied.  An LDS row's 16-byte pieces are permuted by an XOR with its row
-// number, which is applied to the memory address a lane reads (a lane's place
-// in LDS is fixed) and again when the fragments are read, so that the rows a
-// fragment takes lie in different banks.  Lanes outside the operand read
-// through a buffer descriptor at an offset beyond its end, which yields zeros.
+// registers in between).  An LDS row's 16-byte pieces are permuted by an XOR
+// with its row number, which is applied to the memory address a lane reads (a
+// lane's place in LDS is fixed) and again when the fragments are read, so that
+// the rows a fragment takes lie in different banks (no conflict is counted).
+// Lanes outside the operand read through a buffer descriptor at an offset
+// beyond its end, which yields zeros.
+//
+// TileProduct halves each operand's tile and orders a step as four phases, one
+// a pair of halves, so that every phase multiplies what stands in registers while
+// the half that the next phase needs is read from LDS and the same half of the step
+// after the next is loaded into the place that was read last: the loads have one
+// to two steps to arrive, two barriers a step hand places over, and the second
+// step's Q halves come in the other order so that no fragment is read twice.
+//
+// What bounds it (256 x 256, long k, random data): the power budget.  From
+// registers alone the matrix cores run at 2.39 PFLOP/s on zeros and 2.02 on
+// random data; with LDS and memory the clock settles at 1.9 to 2.1 GHz and the
+// products run at 1.3 to 1.4 PFLOP/s, 56 to 68% of the cycles on the matrix cores (a
+// library product of 8192 x 2048 x 128000: 1.40).  Measured on the way (dw of 8192 x 2048
+// x 128000, eight chunks): one read-multiply-barrier loop 448 us a chunk; the reads of
+// one half step under the products of the other 423; phases with few scalar
+// instructions a load and 8 waves 408, with 4 waves of 128 x 128, which
+// read a third less LDS, 375.  With 4 waves the sums stand in
+// accumulation registers through products written in assembly: left to the
+// compiler they moved and spilled (1430 us).  A workgroup that runs on to its next tile
+// with that tile's first loads in flight changed nothing (13.2 against 13.0 ms).
 #pragma once
 
 #include "lm.hpp"
