@@ -148,7 +148,7 @@ __global__ __launch_bounds__(T::THREADS) void ce_stats_kernel(const CeArgs a, in
 // Joins the tiles' maxima and sums of each token: 16 tokens a workgroup, 64
 // lanes each, eight loads of a lane at a time.
 __global__ __launch_bounds__(1024) void ce_join_kernel(const CeArgs a, int parts) {
-    __shared__ float2 buf[64][17];
+    __shared__ float2 buf[16][17];
     const int c = threadIdx.x & 15, l = threadIdx.x >> 4, tok = blockIdx.x * 16 + c;
     float2 s = make_float2(-__builtin_inff(), 0.0f);
     if (tok < a.n)
@@ -161,12 +161,14 @@ __global__ __launch_bounds__(1024) void ce_join_kernel(const CeArgs a, int parts
 #pragma unroll
             for (int k = 0; k < 8; ++k) s = join(s, o[k]);
         }
-    buf[l][c] = s;
+    // four of a wave's lanes share a token, then the 16 waves do
+    s = join(s, make_float2(__shfl_xor(s.x, 16), __shfl_xor(s.y, 16)));
+    s = join(s, make_float2(__shfl_xor(s.x, 32), __shfl_xor(s.y, 32)));
+    if ((l & 3) == 0) buf[l >> 2][c] = s;
     __syncthreads();
-    for (int o = 32; o > 0; o >>= 1) {
-        if (l < o) buf[l][c] = s = join(s, buf[l + o][c]);
-        __syncthreads();
-    }
+    if (l == 0)
+#pragma unroll
+        for (int i = 1; i < 16; ++i) s = join(s, buf[i][c]);
     if (l == 0 && tok < a.n) {
         const float base = fabsf(s.x) == __builtin_inff() ? 0.0f : s.x;
         const float more = __builtin_amdgcn_logf(s.y);
@@ -723,7 +725,7 @@ hipError_t launch_ce_bwd(const CeArgs& args, hipStream_t s) {
         }
     }
     const int64_t quads = (int64_t)a.n * a.d / 4;
-    if (used >= 8) LRS_LAUNCH(K_LM_CE_JOIN, ce_dh_join_kernel<8>, dim3((unsigned)ceil_div(quads, 32)), dim3(256), 0, s, a, used);
+    if (used >= 16) LRS_LAUNCH(K_LM_CE_JOIN, ce_dh_join_kernel<8>, dim3((unsigned)ceil_div(quads, 32)), dim3(256), 0, s, a, used);
     else LRS_LAUNCH(K_LM_CE_JOIN, ce_dh_join_kernel<1>, dim3((unsigned)ceil_div(quads, 256)), dim3(256), 0, s, a, used);
     return hipGetLastError();
 }

@@ -339,7 +339,7 @@ __global__ __launch_bounds__(L > 0 ? 256 : 1024) void norm_bwd_kernel(const Norm
 __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* part, int blocks, int d, const float* w_post,
                                                            const float* scale, float* dw_post, float* dscale,
                                                            float* dw_pre) {
-    __shared__ double buf[64][17];
+    __shared__ double buf[16][17];
     const int c = threadIdx.x & 15, lane = threadIdx.x >> 4, col = blockIdx.x * 16 + c, k = blockIdx.y;
     double s = 0.0;
     if (col < d)
@@ -350,14 +350,15 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* part, in
 #pragma unroll
             for (int u = 0; u < 8; ++u) s += (double)v[u];
         }
-    buf[lane][c] = s;
+    // four of a wave's lanes share a column, then the 16 waves do
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if ((lane & 3) == 0) buf[lane >> 2][c] = s;
     __syncthreads();
-    for (int o = 32; o > 0; o >>= 1) {
-        if (lane < o) buf[lane][c] += buf[lane + o][c];
-        __syncthreads();
-    }
     if (lane == 0 && col < d) {
-        const double v = buf[0][c];
+        double v = buf[0][c];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) v += buf[i][c];
         if (k == 0) {
             dw_pre[col] = (float)v;
         } else {
