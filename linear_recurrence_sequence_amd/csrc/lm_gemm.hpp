@@ -131,7 +131,7 @@ struct TileProduct {
             asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds"
                          :
                          : "s"(to), "s"(at + WAVES * 1024 * j), "v"(o), "s"(rsrc)
-                         : "memory", "scc");
+                         : "memory", "scc", "m0");
         }
         __device__ __forceinline__ void request_half(int at, int h) {
 #pragma unroll
@@ -359,7 +359,7 @@ struct ThinProduct {
             asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                          :
                          : "s"((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char*)to), "v"(o), "s"(rsrc)
-                         : "memory");
+                         : "memory", "m0");
         }
         // requests the tile of one step into LDS; left: reduction indices left (64 or more, but in the last step)
         __device__ __forceinline__ void request(char* lds, int left) {
