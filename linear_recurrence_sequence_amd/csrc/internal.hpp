@@ -7,9 +7,9 @@
 #include <stddef.h>
 #include <stdint.h>
 
-namespace lrs {
+#include "ints.hpp"
 
-__host__ __device__ constexpr inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+namespace lrs {
 
 // ------------------------------------------------------------ profiler ---
 // When enabled, every kernel launch is bracketed by a pair of HIP events on

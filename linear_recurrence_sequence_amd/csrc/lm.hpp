@@ -144,14 +144,6 @@ struct CeArgs {
     int grad_f32;
     int few;                    // columns of dz laid out [chunk, few]; 0: [active, chunk]
 };
-struct CePlan {
-    int chunk;   // vocabulary entries a backward pass takes at a time (a multiple of 256)
-    int splits;  // ranges of a chunk summed apart for dh
-    int dh;      // tile shape of its product
-    int few;     // columns of a transposed dz (32, 64, 128 or 256), 0 with many tokens
-};
-int ce_parts(int n, int d, int v);
-CePlan ce_plan(int n, int d, int v);
 hipError_t launch_ce_fwd(const CeArgs& a, hipStream_t s);
 hipError_t launch_ce_bwd(const CeArgs& a, hipStream_t s);
 

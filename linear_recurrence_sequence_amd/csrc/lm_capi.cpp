@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "lm.hpp"
+#include "lm_ce_plan.hpp"
 #include "lm_ops.h"
 
 namespace lrs {

@@ -18,6 +18,7 @@
 // backward): 8192 x 2048 x 128000 forward + backward 12.8 ms, 1.35 PFLOP/s, where
 // four library products of the shape alone take 13.2; by reading w, and writing
 // dw, for few: 16 x 1024 x 32000 forward 12.5 us, 5.2 TB/s, and a second launch.
+#include "lm_ce_plan.hpp"
 #include "lm_gemm.hpp"
 
 namespace lrs {
@@ -546,91 +547,12 @@ template <bool PT, bool QT>
 using Small = TileProduct<128, 128, 2, 2, PT, QT>;
 template <bool PT, bool QT>
 using Few = ThinProduct<64, 32, 4, 1, PT, QT>;
-
-enum Shape { LARGE, SMALL, FEW };
-constexpr int kBM[3] = {256, 128, 64}, kBN[3] = {256, 128, 32};
-
-constexpr int kFew = 256;  // tokens up to which the backward goes by the bytes of w and dw
-constexpr int64_t kMostDz = (int64_t)128 << 20;  // elements of dz held at once
-
-// Time of a product of p x q results over k, in microseconds: rounds of
-// workgroups, each its steps of 64 and the start and end of a tile.  A large tile's step
-// takes 1.45 us and its start and end 6; two small ones of a CU 1.0 and 5, and one
-// alone 0.7 (measured over long and short k with the CUs busy).
-double product_us(Shape s, int64_t p, int64_t q, int64_t k) {
-    const int64_t tiles = ceil_div(p, kBM[s]) * ceil_div(q, kBN[s]);
-    const double steps = (double)ceil_div(k, GEMM_BK);
-    if (s == LARGE) return (double)ceil_div(tiles, 256) * (steps * 1.45 + 6.0);
-    const int64_t rest = tiles % 512;
-    return (double)(tiles / 512) * (steps + 5.0) + (rest == 0 ? 0.0 : rest <= 256 ? steps * 0.7 + 5.0 : steps + 5.0);
-}
-
-// How many of `rows` vocabulary entries go by large tiles, against `other` rows
-// over k: all, none, or the whole rounds of them, the rest then going by small
-// tiles in a launch of its own (486 x 2384 x 33847 is 266 large tiles, ten more than a
-// round).  A multiple of 256, or all.
-int64_t large_rows(int64_t rows, int64_t other, int64_t k, double* us = nullptr) {
-    const int64_t across = ceil_div(other, 256), whole = ceil_div(rows, 256) * across / 256 * 256 / across * 256;
-    int64_t best = 0;
-    double least = product_us(SMALL, rows, other, k);
-    for (int64_t large : {rows, whole}) {
-        if (large <= 0 || large > rows) continue;
-        // two launches have to be worth a tenth
-        const double t = large == rows ? product_us(LARGE, rows, other, k)
-                                       : 1.1 * (product_us(LARGE, large, other, k) + product_us(SMALL, rows - large, other, k) + 3.0);
-        if (t <= least) least = t, best = large;
-    }
-    if (us) *us = least;
-    return best;
-}
+template <class T>
+constexpr bool is_shape(Shape s) { return T::TILE_P == kBM[s] && T::TILE_Q == kBN[s]; }
+static_assert(is_shape<Wide<false, false>>(LARGE) && is_shape<Large<true, true>>(LARGE) && is_shape<Small<true, true>>(SMALL) &&
+              is_shape<Few<true, true>>(FEW) && CE_STEP == GEMM_BK, "the plan's tiles");
 
 }  // namespace
-
-int ce_parts(int n, int d, int v) {
-    if (n <= 32) return (int)ceil_div(v, kBM[FEW]);
-    const int64_t large = large_rows(v, n, d);
-    return (int)(ceil_div(large, 256) + ceil_div(v - large, 128));
-}
-
-// Chunks of the vocabulary, tiles and the ranges that dh is summed over: the
-// cheapest by product_us and the bytes of dh's partial sums, over the chunk
-// counts from the least that the buffer of dz allows.
-CePlan ce_plan(int n, int d, int v) {
-    n = std::max(n, 1);
-    if (n <= kFew) {
-        CePlan p{};
-        p.few = n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
-        const int64_t chunks = ceil_div(v, kMostDz / p.few / 256 * 256);
-        p.chunk = (int)(ceil_div(ceil_div(v, chunks), 256) * 256);
-        p.dh = n <= 32 ? FEW : SMALL;
-        // the product over the vocabulary reads w once: enough ranges to fill the chip, four steps or more each
-        const int64_t tiles = ceil_div(d, kBM[p.dh]) * ceil_div(n, kBN[p.dh]), want = (p.dh == FEW ? 1024 : 512) / tiles;
-        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(want, std::min(p.chunk, v) / (4 * GEMM_BK)));
-        return p;
-    }
-    const int64_t most = std::max<int64_t>(256, kMostDz / n / 256 * 256), least = ceil_div(v, most);
-    CePlan best{};
-    double best_us = 0.0;
-    for (int64_t chunks = least; chunks < least + 8; ++chunks) {
-        const int64_t chunk = ceil_div(ceil_div(v, chunks), 256) * 256, count = std::min<int64_t>(chunk, v);
-        CePlan p{};
-        p.chunk = (int)chunk;
-        double us, dw_us, dh_us = 0.0;
-        large_rows(count, n, d, &us);
-        large_rows(count, d, n, &dw_us);
-        us += dw_us;
-        for (int s = LARGE; s <= SMALL; ++s) {
-            for (int splits = 1; splits <= 64 && (splits == 1 || count / splits >= 8 * GEMM_BK); ++splits) {
-                // the partial sums are written, and read by the next chunk or the last launch
-                const double t = product_us((Shape)s, d, ceil_div(n, kBN[s]) * kBN[s] * splits, ceil_div(count, splits)) + (double)splits * n * d * 8 / 4.5e6;
-                if (dh_us == 0.0 || t < dh_us) dh_us = t, p.dh = s, p.splits = splits;
-            }
-        }
-        us = (us + dh_us) * (double)ceil_div(v, chunk);
-        if (best_us == 0.0 || us < best_us) best_us = us, best = p;
-    }
-    return best;
-}
 
 #define CE_SHAPES(shape, ID, GRID, KERNEL, BIG, PT, QT, ...)                                                                    \
     do {                                                                                                                       \
@@ -697,7 +619,7 @@ hipError_t launch_ce_bwd(const CeArgs& args, hipStream_t s) {
         }
         {
             const int np = (int)ceil_div(a.d, kBM[pl.dh]);
-            const int range = (int)(ceil_div(ceil_div(count, pl.splits), GEMM_BK) * GEMM_BK), splits = (int)ceil_div(count, range);
+            const auto [range, splits] = ce_ranges(pl, count);
             if (v0 == 0) used = splits;
             const dim3 g((unsigned)(np * ceil_div(a.n, kBN[pl.dh]) * splits));
             if (pl.dh == LARGE) LRS_LAUNCH(K_LM_CE_DH, (ce_dh_kernel<Large<true, false>>), g, dim3(Large<true, false>::THREADS), 0, s, a, np, v0, count, ld, range, splits, v0 == 0);
