@@ -600,7 +600,6 @@ hipError_t launch_ce_bwd(const CeArgs& args, hipStream_t s) {
         LRS_LAUNCH(K_LM_CE_LIST, ce_list_kernel, dim3(1), dim3(1024), 0, s, a);
         LRS_LAUNCH(K_LM_CE_LIST, ce_pack_kernel, dim3((unsigned)ceil_div(a.n, 4)), dim3(256), 0, s, a);
     }
-    int used = 1;  // ranges of the first chunk, which is the longest
     for (int v0 = 0; v0 < a.v; v0 += pl.chunk) {
         const int count = std::min(pl.chunk, a.v - v0), ld = pl.chunk;
         const auto part_of = [&](int at) {  // the arguments with dz from entry `at` of the chunk on
@@ -620,7 +619,6 @@ hipError_t launch_ce_bwd(const CeArgs& args, hipStream_t s) {
         {
             const int np = (int)ceil_div(a.d, kBM[pl.dh]);
             const auto [range, splits] = ce_ranges(pl, count);
-            if (v0 == 0) used = splits;
             const dim3 g((unsigned)(np * ceil_div(a.n, kBN[pl.dh]) * splits));
             if (pl.dh == LARGE) LRS_LAUNCH(K_LM_CE_DH, (ce_dh_kernel<Large<true, false>>), g, dim3(Large<true, false>::THREADS), 0, s, a, np, v0, count, ld, range, splits, v0 == 0);
             else if (!pl.few) LRS_LAUNCH(K_LM_CE_DH, (ce_dh_kernel<Small<true, false>>), g, dim3(Small<true, false>::THREADS), 0, s, a, np, v0, count, ld, range, splits, v0 == 0);
@@ -647,8 +645,8 @@ hipError_t launch_ce_bwd(const CeArgs& args, hipStream_t s) {
         }
     }
     const int64_t quads = (int64_t)a.n * a.d / 4;
-    if (used >= 16) LRS_LAUNCH(K_LM_CE_JOIN, ce_dh_join_kernel<8>, dim3((unsigned)ceil_div(quads, 32)), dim3(256), 0, s, a, used);
-    else LRS_LAUNCH(K_LM_CE_JOIN, ce_dh_join_kernel<1>, dim3((unsigned)ceil_div(quads, 256)), dim3(256), 0, s, a, used);
+    if (pl.splits >= 16) LRS_LAUNCH(K_LM_CE_JOIN, ce_dh_join_kernel<8>, dim3((unsigned)ceil_div(quads, 32)), dim3(256), 0, s, a, pl.splits);
+    else LRS_LAUNCH(K_LM_CE_JOIN, ce_dh_join_kernel<1>, dim3((unsigned)ceil_div(quads, 256)), dim3(256), 0, s, a, pl.splits);
     return hipGetLastError();
 }
 

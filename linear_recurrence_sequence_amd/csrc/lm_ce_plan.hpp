@@ -57,10 +57,19 @@ inline int ce_parts(int n, int d, int v) {
 
 struct CePlan {
     int chunk;   // vocabulary entries a backward pass takes at a time (a multiple of 256)
-    int splits;  // ranges of a chunk summed apart for dh
+    int splits;  // ranges of a chunk summed apart for dh, at most
+    int range;   // entries of a range, a whole number of steps
     int dh;      // tile shape of its product
     int few;     // columns of a transposed dz (32, 64, 128 or 256), 0 with many tokens
 };
+
+// The range that cuts a chunk of `count` entries into about `splits`, and how many it makes.  It is formed once, from the
+// first chunk, which is the longest, and holds for all: rounding to whole steps is not monotone, so that a range of its own could cut a
+// shorter chunk into more pieces than the workspace holds and the last launch sums.
+inline void ce_set_range(CePlan& p, int64_t count) {
+    p.range = (int)(ceil_div(ceil_div(count, p.splits), CE_STEP) * CE_STEP);
+    p.splits = (int)ceil_div(count, p.range);
+}
 
 // Chunks of the vocabulary, tiles and the ranges that dh is summed over: the
 // cheapest by product_us and the bytes of dh's partial sums, over the chunk
@@ -76,6 +85,7 @@ inline CePlan ce_plan(int n, int d, int v) {
         // the product over the vocabulary reads w once: enough ranges to fill the chip, four steps or more each
         const int64_t tiles = ceil_div(d, kBM[p.dh]) * ceil_div(n, kBN[p.dh]), want = (p.dh == FEW ? 1024 : 512) / tiles;
         p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(want, std::min(p.chunk, v) / (4 * CE_STEP)));
+        ce_set_range(p, std::min(p.chunk, v));
         return p;
     }
     const int64_t most = std::max<int64_t>(256, kMostDz / n / 256 * 256), least = ceil_div(v, most);
@@ -99,16 +109,14 @@ inline CePlan ce_plan(int n, int d, int v) {
         us = (us + dh_us) * (double)ceil_div(v, chunk);
         if (best_us == 0.0 || us < best_us) best_us = us, best = p;
     }
+    ce_set_range(best, std::min(best.chunk, v));
     return best;
 }
 
-// The ranges that dh's sum over a chunk of `count` entries is cut into: entries of each, a whole number of steps, and how many.
+// The ranges that dh's sum over a chunk of `count` entries is cut into: entries of each, and how many.
 struct CeRanges {
     int range, splits;
 };
-inline CeRanges ce_ranges(const CePlan& p, int count) {
-    const int range = (int)(ceil_div(ceil_div(count, p.splits), CE_STEP) * CE_STEP);
-    return {range, (int)ceil_div(count, range)};
-}
+inline CeRanges ce_ranges(const CePlan& p, int count) { return {p.range, (int)ceil_div(count, p.range)}; }
 
 }  // namespace lrs

@@ -1,0 +1,52 @@
+// Walks the linear cross entropy's plan as its launches do, over sizes across
+// the whole accepted range: what a chunk of the vocabulary writes has to be what
+// the last launch sums, inside the workspace.  Host arithmetic; no GPU.
+#include <stdio.h>
+#include <stdlib.h>
+
+#include <cmath>
+#include <random>
+
+#include "lm_ce_plan.hpp"
+
+using namespace lrs;
+
+static long long several, worst_chunks;
+
+static void fail(const char* what, int n, int d, int v) {
+    printf("%s: n=%d d=%d v=%d\n", what, n, d, v);
+    exit(1);
+}
+
+static void walk(int n, int d, int v) {
+    const CePlan p = ce_plan(n, d, v);
+    if (p.chunk < 256 || p.chunk % 256 || p.splits < 1 || (p.few ? n > p.few : n <= 256)) fail("plan", n, d, v);
+    const int64_t chunks = ceil_div(v, p.chunk), last = v - (chunks - 1) * p.chunk;
+    const int first = std::min(p.chunk, v), used = ce_ranges(p, first).splits;
+    if (used > p.splits) fail("more ranges than the workspace holds", n, d, v);
+    for (int count : {first, (int)last}) {
+        const CeRanges r = ce_ranges(p, count);
+        if (r.range < CE_STEP || r.range % CE_STEP || r.splits < 1) fail("range", n, d, v);
+        if ((int64_t)r.range * r.splits < count || (int64_t)r.range * (r.splits - 1) >= count) fail("ranges do not cover the chunk", n, d, v);
+        if (r.splits > used) fail("a chunk has more ranges than are summed", n, d, v);
+    }
+    several += chunks > 1;
+    worst_chunks = std::max<long long>(worst_chunks, chunks);
+}
+
+int main(int argc, char** argv) {
+    const int rounds = argc > 1 ? atoi(argv[1]) : 10000;
+    const int seen[][3] = {{141, 72, 557087}, {206, 304, 674427}, {80, 400, 2605384}, {200, 64, 589826}, {247, 200, 589971}, {91, 264, 1066594},
+                           {1, 8, 1}, {32, 8, 0x7fffffff - 513}, {256, 65536, 0x7fffffff - 513}, {257, 8, 1 << 22}, {8192, 2048, 128000}};
+    for (const auto& s : seen) walk(s[0], s[1], s[2]);
+    std::mt19937_64 rng(1);
+    const auto spread = [&](double lo, double hi) { return (int)std::exp(std::uniform_real_distribution<>(std::log(lo), std::log(hi))(rng)); };
+    for (int i = 0; i < rounds; ++i) {
+        walk(spread(1, 257), 8 * spread(1, 1024), spread(3e5, 2e7));   // few tokens, about one chunk and more
+        walk(spread(129, 257), 8 * spread(1, 64), spread(5e5, 3e6));
+        walk(spread(257, 20000), 8 * spread(1, 1024), spread(1, 1e6));
+        walk(spread(1, 20000), 8 * spread(1, 64), spread(1, 4e6));
+    }
+    printf("%lld of several chunks, at most %lld; all walked\n", several, worst_chunks);
+    return 0;
+}
