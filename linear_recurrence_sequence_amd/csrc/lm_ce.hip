@@ -38,11 +38,12 @@ __device__ __forceinline__ void tile_of(int np, int nq, int b, int* p, int* q) {
     *p = in / size;
 }
 
-// tanh(z / cap) of four logits, in place.  Up to |x| = 1 the continued fraction
+// tanh(z / cap) of four logits, in place, and its slope 1 - tanh^2.  Up to |x| = 1 the continued fraction
 // x / (1 + x^2 / (3 + x^2 / (5 + ...))) to its sixth denominator, off by less than FP32's own
-// rounding there; beyond, which a wave seldom meets, 1 - 2 / (1 + e^2x), which near zero would
-// keep the rounding of 1.
-__device__ __forceinline__ void cap_tanh(f32acc_t& z, float inv_cap) {
+// rounding there; beyond, which a wave seldom meets, 1 - 2 q with q = 1 / (1 + e^2|x|), which near zero would
+// keep the rounding of 1.  There the slope is 4 q (1 - q): formed from a tanh already rounded near 1 it would be off by
+// 0.7% at |x| = 6.5 and zero from 9 on, where it is 6e-8.
+__device__ __forceinline__ void cap_tanh(f32acc_t& z, f32acc_t& slope, float inv_cap) {
     float top = 0.0f;
     f32acc_t x, y;
 #pragma unroll
@@ -52,11 +53,16 @@ __device__ __forceinline__ void cap_tanh(f32acc_t& z, float inv_cap) {
         top = fmaxf(top, y[r]);
         z[r] = x[r] * fmaf(fmaf(21.0f, y[r], 1260.0f), y[r], 10395.0f) *
                __builtin_amdgcn_rcpf(fmaf(fmaf(y[r] + 210.0f, y[r], 4725.0f), y[r], 10395.0f));
+        slope[r] = (1.0f - z[r]) * (1.0f + z[r]);
     }
     if (__ballot(top >= 1.0f)) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            if (!(y[r] < 1.0f)) z[r] = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(2.0f * LOG2E * x[r]));
+            if (!(y[r] < 1.0f)) {
+                const float q = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(2.0f * LOG2E * fabsf(x[r])));
+                z[r] = copysignf(1.0f - 2.0f * q, x[r]);
+                slope[r] = 4.0f * q * (1.0f - q);
+            }
     }
 }
 
@@ -93,9 +99,9 @@ __global__ __launch_bounds__(T::THREADS) void ce_stats_kernel(const CeArgs a, in
 #pragma unroll
         for (int j = 0; j < T::FN; ++j)
 #pragma unroll
-            for (int i = 0; i < T::FM; ++i)
-            {
-                cap_tanh(t.acc[i][j], inv_cap);
+            for (int i = 0; i < T::FM; ++i) {
+                f32acc_t slope;
+                cap_tanh(t.acc[i][j], slope, inv_cap);
                 t.acc[i][j] *= a.cap;
             }
     }
@@ -307,7 +313,8 @@ __global__ __launch_bounds__(T::THREADS) void ce_dz_kernel(const CeArgs a, int n
 #pragma unroll
         for (int i = 0; i < T::FM; ++i) {
             float g[4];
-            if (CAP) cap_tanh(t.acc[i][j], inv_cap);
+            f32acc_t slope;
+            if (CAP) cap_tanh(t.acc[i][j], slope, inv_cap);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 g[r] = __builtin_amdgcn_exp2f(fmaf(t.acc[i][j][r], CAP ? a.cap * LOG2E : LOG2E, -k.base)) * k.c;
@@ -318,7 +325,7 @@ __global__ __launch_bounds__(T::THREADS) void ce_dz_kernel(const CeArgs a, int n
             }
             if (CAP) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) g[r] *= (1.0f - t.acc[i][j][r]) * (1.0f + t.acc[i][j][r]);
+                for (int r = 0; r < 4; ++r) g[r] *= slope[r];
             }
             if (a.few) {
                 if (tok >= m) g[0] = g[1] = g[2] = g[3] = 0.0f;
