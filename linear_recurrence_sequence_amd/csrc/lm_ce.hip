@@ -607,8 +607,9 @@ hipError_t launch_ce_bwd(const CeArgs& args, hipStream_t s) {
         LRS_LAUNCH(K_LM_CE_LIST, ce_list_kernel, dim3(1), dim3(1024), 0, s, a);
         LRS_LAUNCH(K_LM_CE_LIST, ce_pack_kernel, dim3((unsigned)ceil_div(a.n, 4)), dim3(256), 0, s, a);
     }
-    for (int v0 = 0; v0 < a.v; v0 += pl.chunk) {
-        const int count = std::min(pl.chunk, a.v - v0), ld = pl.chunk;
+    for (int i = 0; i < ce_chunks(pl, a.v); ++i) {
+        const CeChunk ch = ce_chunk(pl, a.v, i);
+        const int v0 = ch.first, count = ch.count, splits = ch.splits, range = pl.range, ld = pl.chunk;
         const auto part_of = [&](int at) {  // the arguments with dz from entry `at` of the chunk on
             CeArgs p = a;
             p.dz = static_cast<uint16_t*>(a.dz) + (int64_t)at * (a.few ? a.few : 1);
@@ -625,7 +626,6 @@ hipError_t launch_ce_bwd(const CeArgs& args, hipStream_t s) {
         }
         {
             const int np = (int)ceil_div(a.d, kBM[pl.dh]);
-            const auto [range, splits] = ce_ranges(pl, count);
             const dim3 g((unsigned)(np * ceil_div(a.n, kBN[pl.dh]) * splits));
             if (pl.dh == LARGE) LRS_LAUNCH(K_LM_CE_DH, (ce_dh_kernel<Large<true, false>>), g, dim3(Large<true, false>::THREADS), 0, s, a, np, v0, count, ld, range, splits, v0 == 0);
             else if (!pl.few) LRS_LAUNCH(K_LM_CE_DH, (ce_dh_kernel<Small<true, false>>), g, dim3(Small<true, false>::THREADS), 0, s, a, np, v0, count, ld, range, splits, v0 == 0);

@@ -113,10 +113,14 @@ inline CePlan ce_plan(int n, int d, int v) {
     return best;
 }
 
-// The ranges that dh's sum over a chunk of `count` entries is cut into: entries of each, and how many.
-struct CeRanges {
-    int range, splits;
+// Chunk i of the vocabulary: its first entry, its entries, and the ranges that dh's sum over it is cut into.
+struct CeChunk {
+    int first, count, splits;
 };
-inline CeRanges ce_ranges(const CePlan& p, int count) { return {p.range, (int)ceil_div(count, p.range)}; }
+inline int ce_chunks(const CePlan& p, int v) { return (int)ceil_div(v, p.chunk); }
+inline CeChunk ce_chunk(const CePlan& p, int v, int i) {
+    const int64_t first = (int64_t)i * p.chunk, count = std::min<int64_t>(p.chunk, v - first);  // first + chunk may pass 2^31
+    return {(int)first, (int)count, (int)ceil_div(count, p.range)};
+}
 
 }  // namespace lrs

@@ -21,15 +21,19 @@ static void fail(const char* what, int n, int d, int v) {
 static void walk(int n, int d, int v) {
     const CePlan p = ce_plan(n, d, v);
     if (p.chunk < 256 || p.chunk % 256 || p.splits < 1 || (p.few ? n > p.few : n <= 256)) fail("plan", n, d, v);
-    const int64_t chunks = ceil_div(v, p.chunk), last = v - (chunks - 1) * p.chunk;
-    const int first = std::min(p.chunk, v), used = ce_ranges(p, first).splits;
-    if (used > p.splits) fail("more ranges than the workspace holds", n, d, v);
-    for (int count : {first, (int)last}) {
-        const CeRanges r = ce_ranges(p, count);
-        if (r.range < CE_STEP || r.range % CE_STEP || r.splits < 1) fail("range", n, d, v);
-        if ((int64_t)r.range * r.splits < count || (int64_t)r.range * (r.splits - 1) >= count) fail("ranges do not cover the chunk", n, d, v);
-        if (r.splits > used) fail("a chunk has more ranges than are summed", n, d, v);
+    const int chunks = ce_chunks(p, v);
+    int64_t next = 0;
+    for (int i = 0; i < chunks; ++i) {
+        // of very many chunks the first and the last ones
+        if (i == 1000 && chunks > 2000) next = (int64_t)p.chunk * (i = chunks - 1000);
+        const CeChunk c = ce_chunk(p, v, i);
+        if (c.first != next || c.count < 1 || c.count > p.chunk) fail("chunks do not follow each other", n, d, v);
+        next += c.count;
+        if (p.range < CE_STEP || p.range % CE_STEP || c.splits < 1) fail("range", n, d, v);
+        if ((int64_t)p.range * c.splits < c.count || (int64_t)p.range * (c.splits - 1) >= c.count) fail("ranges do not cover the chunk", n, d, v);
+        if (c.splits > p.splits) fail("a chunk has more ranges than are summed", n, d, v);
     }
+    if (next != v) fail("chunks do not cover the vocabulary", n, d, v);
     several += chunks > 1;
     worst_chunks = std::max<long long>(worst_chunks, chunks);
 }
@@ -37,7 +41,7 @@ static void walk(int n, int d, int v) {
 int main(int argc, char** argv) {
     const int rounds = argc > 1 ? atoi(argv[1]) : 10000;
     const int seen[][3] = {{141, 72, 557087}, {206, 304, 674427}, {80, 400, 2605384}, {200, 64, 589826}, {247, 200, 589971}, {91, 264, 1066594},
-                           {1, 8, 1}, {32, 8, 0x7fffffff - 513}, {256, 65536, 0x7fffffff - 513}, {257, 8, 1 << 22}, {8192, 2048, 128000}};
+                           {1, 8, 1}, {32, 8, 0x7fffffff - 513}, {256, 65536, 0x7fffffff - 513}, {257, 8, 1 << 22}, {700000, 8, 0x7fffffff - 513}, {8192, 2048, 128000}};
     for (const auto& s : seen) walk(s[0], s[1], s[2]);
     std::mt19937_64 rng(1);
     const auto spread = [&](double lo, double hi) { return (int)std::exp(std::uniform_real_distribution<>(std::log(lo), std::log(hi))(rng)); };
