@@ -86,8 +86,8 @@ scan_status lm_block_norm_bwd(int64_t rows, int d, int stream_dtype, int branch_
  *   h       bf16 [n, d], row stride h_stride (a multiple of 8)
  *   w       bf16 [v, d]
  *   target  int64 [n]
- * 0 <= n, 1 <= v, both < 2^31 - 512, n v < 2^45; 8 <= d <= 65536, a multiple of 8; h and w
- * 16-byte aligned.  The backward works on the tokens with a weight alone
+ * 0 <= n <= 2^26 - 16, 1 <= v < 2^31 - 513, n v < 2^45; 8 <= d <= 65536, a multiple of 8;
+ * n d <= 2^34 - 1024; h and w 16-byte aligned.  The backward works on the tokens with a weight alone
  * (dloss of a token that counts, or dlse, not zero): the others cost it nothing, and
  * whatever their hidden rows hold, NaN and infinities too, stays out of dw.
  * ====================================================================== */

@@ -116,15 +116,10 @@ size_t ce_layout(bool bwd, int n, int d, int v, void* base, CeArgs* a) {
     return std::max<size_t>(off, 256);
 }
 
-bool ce_shape(int64_t n, int d, int64_t v) {
-    return n >= 0 && n < 0x7fffffff - 512 && v >= 1 && v < 0x7fffffff - 512 && d >= 8 && d <= 65536 && d % 8 == 0 &&
-           ceil_div(n, 128) * ceil_div(v, 128) < 0x7fffffff;  // the smaller tiles of a grid
-}
-
 scan_status ce_check(const char* fn, int64_t n, int d, int64_t v, double cap, int64_t h_stride) {
     if (!ce_shape(n, d, v))
         return fail(SCAN_ERR_SHAPE, std::string(fn) + ": unsupported shape n=" + std::to_string(n) + " d=" + std::to_string(d) +
-                                        " v=" + std::to_string(v) + " (need v >= 1, 8 <= d <= 65536 a multiple of 8)");
+                                        " v=" + std::to_string(v) + " (need v >= 1, 8 <= d <= 65536 a multiple of 8, n <= 2^26 - 16, n d <= 2^34 - 1024)");
     if (!(cap >= 0.0) || !std::isfinite((float)cap) || (cap > 0.0 && (float)cap < 1e-30f))
         return fail(SCAN_ERR_SHAPE, std::string(fn) + ": softcap must be 0 (none) or a positive number");
     if (n > 0 && (h_stride % 8 != 0 || h_stride < 0 || h_stride > kMaxCeStride))
@@ -350,9 +345,9 @@ scan_status lm_adamw_step(int count, int param_dtype, int grad_dtype, int state_
     a.eps = (float)eps;
     a.count = 0;
     uint64_t blocks = 0;
-    // a launch holds ADAMW_LAUNCH tensors and at most 2^30 workgroups; a
+    // a launch holds ADAMW_LAUNCH tensors and workgroups of 256 threads; a
     // tensor that does not fit what is left of them is cut at a whole chunk
-    constexpr uint64_t kMost = (uint64_t)1 << 30;
+    constexpr uint64_t kMost = MOST_THREADS / 256;
     auto flush = [&]() -> hipError_t {
         if (a.count == 0) return hipSuccess;
         const hipError_t e = launch_adamw(a, (uint32_t)blocks, param_dtype == SCAN_F32, grad_dtype == SCAN_F32,

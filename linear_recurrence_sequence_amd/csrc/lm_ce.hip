@@ -538,8 +538,7 @@ __global__ __launch_bounds__(256) void ce_dw_few_kernel(const CeArgs a, int vfir
 }
 
 __global__ __launch_bounds__(256) void ce_zero_kernel(uint32_t* p, int64_t words) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i < words) p[i] = 0u;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words; i += (int64_t)gridDim.x * 256) p[i] = 0u;
 }
 
 // Tiles.  256 x 256, one workgroup a CU: 8 waves where the tile ends in
@@ -558,6 +557,7 @@ template <class T>
 constexpr bool is_shape(Shape s) { return T::TILE_P == kBM[s] && T::TILE_Q == kBN[s]; }
 static_assert(is_shape<Wide<false, false>>(LARGE) && is_shape<Large<true, true>>(LARGE) && is_shape<Small<true, true>>(SMALL) &&
               is_shape<Few<true, true>>(FEW) && CE_STEP == GEMM_BK, "the plan's tiles");
+static_assert(Small<false, false>::THREADS == 256 && Few<false, false>::THREADS == 256, "threads of a tile that is not large");
 
 }  // namespace
 
@@ -579,7 +579,8 @@ hipError_t launch_ce_fwd(const CeArgs& a, hipStream_t s) {
         const int sh = a.n <= 32 ? FEW : v0 < large ? LARGE : SMALL;
         CeArgs p = a;
         p.w = static_cast<const char*>(a.w) + (int64_t)v0 * a.d * 2;
-        p.v = (sh == LARGE ? large : a.v) - v0;
+        // a launch over the threads that one may have is cut at a whole tile, so that the parts stay numbered by tiles
+        p.v = (int)std::min<int64_t>((sh == LARGE ? large : a.v) - v0, ce_launch_rows((Shape)sh, sh == LARGE ? Wide<false, false>::THREADS : 256, a.n));
         const int np = (int)ceil_div(p.v, kBM[sh]), nq = (int)ceil_div(a.n, kBN[sh]);
         const dim3 g((unsigned)(np * nq));
         if (a.cap > 0.0f) CE_SHAPES(sh, K_LM_CE_STATS, g, CE_STATS_CAP, Wide, false, false, p, np, nq, v0, part);
@@ -596,7 +597,7 @@ hipError_t launch_ce_bwd(const CeArgs& args, hipStream_t s) {
     CeArgs a = args;
     if (a.n == 0) {  // no token: dw is zero, and there is no dh
         const int64_t words = (int64_t)a.v * a.d * (a.grad_f32 ? 4 : 2) / 4;
-        LRS_LAUNCH(K_CLEAR, ce_zero_kernel, dim3((unsigned)ceil_div(words, 256)), dim3(256), 0, s, (uint32_t*)a.dw, words);
+        LRS_LAUNCH(K_CLEAR, ce_zero_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(words, 256), 1 << 16)), dim3(256), 0, s, (uint32_t*)a.dw, words);
         return hipGetLastError();
     }
     const CePlan pl = ce_plan(a.n, a.d, a.v);

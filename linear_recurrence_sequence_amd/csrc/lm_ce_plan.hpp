@@ -55,6 +55,16 @@ inline int ce_parts(int n, int d, int v) {
     return (int)(ceil_div(large, 256) + ceil_div(v - large, 128));
 }
 
+// Vocabulary entries that one launch of a shape's tiles takes against n tokens, a whole number of tiles.
+inline int64_t ce_launch_rows(Shape s, int threads, int64_t n) { return MOST_THREADS / threads / ceil_div(n, kBN[s]) * kBM[s]; }
+
+// Sizes that are taken.  Indices are 31 bits, tiles included; the launches over tokens take up to 64 threads
+// a token, and the one that joins dh a thread for four of its elements.
+inline bool ce_shape(int64_t n, int d, int64_t v) {
+    return n >= 0 && n <= (1 << 26) - 16 && v >= 1 && v < 0x7fffffff - 512 && d >= 8 && d <= 65536 && d % 8 == 0 &&
+           n * d <= 4 * (MOST_THREADS - 255) && ceil_div(n, 128) * ceil_div(v, 128) < 0x7fffffff;
+}
+
 struct CePlan {
     int chunk;   // vocabulary entries a backward pass takes at a time (a multiple of 256)
     int splits;  // ranges of a chunk summed apart for dh, at most
