@@ -105,7 +105,7 @@ struct AdamwArgs {
     int count;
     float b1, c1, b2, c2, step_size, root_scale, eps;  // c = 1 - b; step_size = lr / (1 - b1^t); root_scale = (1 - b2^t)^-1/2
     uint32_t start[ADAMW_LAUNCH];    // first workgroup of each tensor
-    float keep[ADAMW_LAUNCH];        // 1 - lr decay
+    float decay[ADAMW_LAUNCH];       // lr decay
     int64_t n[ADAMW_LAUNCH];
     void* p[ADAMW_LAUNCH];
     const void* g[ADAMW_LAUNCH];

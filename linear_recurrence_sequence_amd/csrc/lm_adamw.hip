@@ -3,7 +3,7 @@
 //
 // For every element (FP32 arithmetic):
 //   m' = b1 m + (1-b1) g,  v' = b2 v + (1-b2) g^2,
-//   p' = p (1 - lr decay) - step_size m' / (sqrt(v') root_scale + eps).
+//   p' = p - (lr decay p + step_size m' / (sqrt(v') root_scale + eps)).
 // 8-bit moments: blocks of 256 consecutive elements hold e4m3 codes and one
 // FP32 scale, max(|.|) / 448.  The second moment is held as its square root,
 // which halves the range its codes have to span; a positive root takes at
@@ -16,6 +16,8 @@
 // reduction over the wave; a wave requests 4 blocks before it uses the first.
 // 0.42 G weights with a BF16 copy and 8-bit moments take 1172 us, 5.75 TB/s; 58 M with
 // 32-bit ones 277 us, 5.97 TB/s (a large copy: 4.7 to 4.9 TB/s).
+#include <float.h>
+
 #include "lm.hpp"
 
 namespace lrs {
@@ -120,7 +122,7 @@ __device__ __forceinline__ void update(const AdamwArgs& a, int t, int64_t base, 
             sv[u] = in ? a.v_scale[t][b] : 0.0f;
         }
     }
-    const float keep = a.keep[t];
+    const float taken = a.decay[t];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t e = first + u * 256 + lane * 4;
@@ -143,7 +145,9 @@ __device__ __forceinline__ void update(const AdamwArgs& a, int t, int64_t base, 
             moments(a, gg[i], &m[i], &v[i], &root[i]);
             // the reciprocal is the hardware's, within one unit in the last place
             const float upd = m[i] * __builtin_amdgcn_rcpf(root[i] * a.root_scale + a.eps);
-            pp[i] = pp[i] * keep - a.step_size * upd;
+            // What is taken is summed first: 1 - lr decay in FP32 would round a small decay to a multiple of 2^-24, the same for every
+            // element and step.  An infinite weight stays so.
+            pp[i] -= fmaf(a.step_size, upd, taken * __builtin_amdgcn_fmed3f(pp[i], -FLT_MAX, FLT_MAX));
         }
         uint32_t em = 0, ev = 0;
         float ns, nr;

@@ -368,7 +368,7 @@ scan_status lm_adamw_step(int count, int param_dtype, int grad_dtype, int state_
             const int64_t k = std::min<int64_t>(left, (int64_t)take * ADAMW_CHUNK);
             const int c = a.count++;
             a.start[c] = (uint32_t)blocks;
-            a.keep[c] = (float)(1.0 - lr * decay[i]);
+            a.decay[c] = (float)(lr * decay[i]);
             a.n[c] = k;
             a.p[c] = (char*)p[i] + done * ps;
             a.g[c] = (const char*)g[i] + done * gs;
