@@ -151,9 +151,30 @@ def rglru_layer(x, w_x, b_x, w_a, b_a, alpha, reset=None, h0=None, *, K=16, G=0)
     return RglruLayer.apply(x, w_x, b_x, w_a, b_a, alpha, reset, h0, K, G)
 
 
+class _Once(torch.autograd.Function):
+    """A gradient as it is, tied to all that it was formed from: differentiating it raises, where it would otherwise count as a
+    constant.  (torch's once_differentiable looks at the cotangents alone, which need not depend on anything.)"""
+
+    @staticmethod
+    def forward(ctx, what, grad, *formed_from):
+        ctx.what = what
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, grad):
+        raise RuntimeError(f"{ctx.what} has no second derivative")
+
+
+def _once(what, grads, *formed_from):
+    """The gradients of a backward, refused a derivative of their own where create_graph asks for one."""
+    if not torch.is_grad_enabled():
+        return grads
+    return tuple(None if g is None else _Once.apply(what, g, *formed_from) for g in grads)
+
+
 class BlockNorm(torch.autograd.Function):
     """Residual sum and norms around a block: (x, y, gate, w_post, scale,
-    w_pre) -> (r, n), as lm.block_norm_fwd."""
+    w_pre) -> (r, n), as lm.block_norm_fwd.  A second derivative raises."""
 
     @staticmethod
     def forward(ctx, x, y, gate, w_post, scale, w_pre, eps, gate_act):
@@ -170,7 +191,8 @@ class BlockNorm(torch.autograd.Function):
         dr = None if dr is None else dr.contiguous()
         dn = None if dn is None else dn.contiguous()
         g = lm.block_norm_bwd(x, y, gate, w_post, scale, w_pre, stats, dr, dn, eps=ctx.eps, gate_act=ctx.gate_act)
-        return (g["dx"], g["dy"], g.get("dgate"), g.get("dw_post"), g.get("dscale"), g["dw_pre"], None, None)
+        grads = (g["dx"], g["dy"], g.get("dgate"), g.get("dw_post"), g.get("dscale"), g["dw_pre"])
+        return (*_once("block_norm", grads, x, y, gate, w_post, scale, w_pre, dr, dn), None, None)
 
 
 def block_norm(x, y, gate, w_post, scale, w_pre, *, eps=1e-6, gate_act="none"):
@@ -181,7 +203,7 @@ def block_norm(x, y, gate, w_post, scale, w_pre, *, eps=1e-6, gate_act="none"):
 
 class LinearCe(torch.autograd.Function):
     """Softmax cross entropy of a linear head: (h, w, target) -> (loss, lse),
-    token by token, as lm.linear_ce_fwd."""
+    token by token, as lm.linear_ce_fwd.  A second derivative raises."""
 
     @staticmethod
     def forward(ctx, h, w, target, softcap):
@@ -198,7 +220,7 @@ class LinearCe(torch.autograd.Function):
             dloss = torch.zeros_like(lse)
         g = lm.linear_ce_bwd(h, w, target, lse, dloss.float().contiguous(), None if dlse is None else dlse.float().contiguous(),
                              softcap=ctx.softcap)
-        return g["dh"], g["dw"], None, None
+        return (*_once("linear_ce", (g["dh"], g["dw"]), h, w, dloss, dlse), None, None)
 
 
 def linear_ce(h, w, target, *, softcap=0.0):
