@@ -51,6 +51,14 @@ __device__ __forceinline__ float sigmoid(float g) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * g));
 }
 
+// s = sigmoid(g) and 1 - s, which of a large g is far smaller than s's own rounding: with e = exp(-g), 1 - s = e s.  An e beyond
+// 2^126, where s is less than FP32 holds, leaves 1.
+__device__ __forceinline__ float sigmoid(float g, float* rest) {
+    const float e = __builtin_amdgcn_exp2f(-1.44269504f * g), s = __builtin_amdgcn_rcpf(1.0f + e);
+    *rest = e > 0x1p126f ? 1.0f : e * s;
+    return s;
+}
+
 // Which elements a lane holds: group c starts at column c * 4 T + 4 t.  Where
 // the width is no multiple of 4 (TAIL) the group that the row ends in is loaded as the
 // row's last four elements and put in place by take(), so that no load stands in a
@@ -272,7 +280,8 @@ __global__ __launch_bounds__(L > 0 ? 256 : 1024) void norm_bwd_kernel(const Norm
                 take<TAIL>(qg[c], c * 4 * T + 4 * t, a.d, f);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float sg = sigmoid(f[i]), slope = sg * (1.0f - sg);
+                    float rest;
+                    const float sg = sigmoid(f[i], &rest), slope = sg * rest;
                     da[i] = v[i] * yh[i] * w1[c][i] * (silu ? sg + f[i] * slope : slope);
                     v[i] *= silu ? sg * f[i] : sg;
                 }
