@@ -151,7 +151,9 @@ scan_status lm_block_norm_fwd(int64_t rows, int d, int stream_dtype, int branch_
         at{stats, (size_t)rows * 8, 4, "stats"};
     st = check_args({ax, ay, a2, ar, an, at}, {ag, a1, as});
     if (st != SCAN_OK) return st;
-    // r may be x itself (every element is read before the same lane writes it)
+    // r may be x itself: all of a row is read before any of it is written.  Not by each lane its own elements (where d is no
+    // multiple of 4 the lane at the row's end reads its neighbour's too), but because r's norm, which needs them all, stands between:
+    // with a barrier where a row is several waves', and a wave's lanes run together.
     const bool in_place = r == x && (x_stride == d || rows == 1);
     st = check_alias({in_place ? Arg{nullptr, 0, 1, "x"} : ax, ay, ag, a1, as, a2}, {ar, an, at});
     if (st != SCAN_OK) return st;
