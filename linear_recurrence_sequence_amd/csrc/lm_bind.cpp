@@ -90,7 +90,12 @@ PyObject *current_device, *current_stream;  // torch's own, set by setup
 void* stream_of(PyObject* o, const c10::Device& dev) {
     PyObject* device = PyObject_CallNoArgs(current_device);
     need(device != nullptr);
-    const bool here = PyLong_AsLong(device) == dev.index();
+    bool here = PyLong_AsLong(device) == dev.index();
+    if (here && o != Py_None) {  // a stream of the same device
+        PyObject* index = PyObject_GetAttrString(o, "device_index");
+        here = index && PyLong_AsLong(index) == dev.index();
+        Py_XDECREF(index);
+    }
     PyObject* raw = !here ? nullptr : o == Py_None ? PyObject_CallOneArg(current_stream, device) : PyObject_GetAttrString(o, "cuda_stream");
     Py_DECREF(device);
     need(raw != nullptr);

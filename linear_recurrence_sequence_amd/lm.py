@@ -8,7 +8,8 @@ the current stream or the one given.  The differentiable forms are in
 autograd.py.
 
 With a stream given a call runs as if that stream were the current one: its
-outputs and workspace are allocated there.
+outputs and workspace are allocated there.  Tensors lie on the current device,
+or the stream's.
 
 A plainly right call with outputs of its own goes through _lm_bind (see
 csrc/lm_bind.cpp), which makes the checks below in a few microseconds; every other call is
@@ -75,10 +76,18 @@ def _p(t):
     return t.data_ptr()
 
 
+def _current(device):
+    """Refuses tensors of another device than the current one: the launch and its stream are the current one's."""
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}: call under "
+                         f"torch.cuda.device, or with a stream of {device}")
+
+
 def _same_device(first, **tensors):
     for name, t in tensors.items():
         if t is not None and t.device != first.device:
             raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+    _current(first.device)
 
 
 def _dense(t, name):
@@ -369,9 +378,14 @@ def adamw_step(params, grads, m, v, *, step, lr, betas=(0.9, 0.999), eps=1e-8, w
         args += [None, None]
     if not p0.is_cuda:
         raise ValueError("expected device tensors")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return adamw_step(params, grads, m, v, step=step, lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, masters=masters,
+                              m_scales=m_scales, v_scales=v_scales)
+    _current(dev)
     st = lib().lm_adamw_step(count, _code(p0.dtype), _code(g0.dtype), bits, *args, (ctypes.c_int64 * count)(*sizes),
                              (ctypes.c_double * count)(*decay), lr, betas[0], betas[1], eps, int(step),
-                             _stream(stream))
+                             _stream(None))
     _check(st, "lm_adamw_step")
 
 
