@@ -294,6 +294,11 @@ struct List {
             at[i] = dense(t, type, dev);
         }
     }
+    // says to autograd that a call wrote the tensors (5 ns each: of a step's, the weights, which graphs keep)
+    void written() const {
+        for (Py_ssize_t i = 0; fast && i < size(); ++i)
+            if (!(*this)[i].is_inference()) (*this)[i].unsafeGetTensorImpl()->bump_version();
+    }
     template <class T>
     T* const* as() {
         return fast ? reinterpret_cast<T* const*>(at.data()) : nullptr;
@@ -338,9 +343,11 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t count) {
         }
         const long long step = PyLong_AsLongLong(a[8]);
         need(!PyErr_Occurred());
-        return status(lm_adamw_step((int)k, code(pt), code(gt), bits8 ? 8 : 32, l[0].as<void>(), l[1].as<const void>(), l[2].as<void>(),
-                                    l[3].as<void>(), l[4].as<float>(), l[5].as<float>(), l[6].as<float>(), n.data(), decay.data(),
-                                    number(a[9]), number(a[10]), number(a[11]), number(a[12]), step, stream_of(a[13], dev)));
+        const scan_status st = lm_adamw_step((int)k, code(pt), code(gt), bits8 ? 8 : 32, l[0].as<void>(), l[1].as<const void>(),
+                                             l[2].as<void>(), l[3].as<void>(), l[4].as<float>(), l[5].as<float>(), l[6].as<float>(),
+                                             n.data(), decay.data(), number(a[9]), number(a[10]), number(a[11]), number(a[12]), step, stream_of(a[13], dev));
+        if (st == SCAN_OK) l[0].written();
+        return status(st);
     });
 }
 

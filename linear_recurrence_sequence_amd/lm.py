@@ -90,6 +90,11 @@ def _same_device(first, **tensors):
     _current(first.device)
 
 
+def _written(*tensors):
+    """Says to autograd that a call wrote tensors of the caller's: a graph that kept one refuses its backward."""
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None and not t.is_inference()])
+
+
 def _dense(t, name):
     if t is not None and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -163,7 +168,7 @@ def block_norm_fwd(x, y, gate, w_post, scale, w_pre, *, eps=1e-6, gate_act="none
         if out is not None:
             _check(out, "lm_block_norm_fwd")
     rows, d, sx, sy, sg = _norm_args(x, y, gate, w_post, scale, w_pre, gate_act)
-    dev = x.device
+    dev, given = x.device, (r, n, stats)
     if r is None:
         r = torch.empty(x.shape, dtype=x.dtype, device=dev)
     else:
@@ -184,6 +189,7 @@ def block_norm_fwd(x, y, gate, w_post, scale, w_pre, *, eps=1e-6, gate_act="none
                                  sx, _p(y), sy, _p(gate), sg, _p(w_post), _p(scale), _p(w_pre), _p(r), _p(n),
                                  _p(stats), _stream(None))
     _check(st, "lm_block_norm_fwd")
+    _written(*given)
     return r, n, stats
 
 
@@ -269,7 +275,7 @@ def linear_ce_fwd(h, w, target, *, softcap=0.0, loss=None, lse=None, workspace=N
         if out is not None:
             _check(out, "lm_linear_ce_fwd")
     n, d, v, sh = _ce_args(h, w, target)
-    dev = h.device
+    dev, given = h.device, (loss, lse)
     out = []
     for t, name in ((loss, "loss"), (lse, "lse")):
         if t is None:
@@ -283,6 +289,7 @@ def linear_ce_fwd(h, w, target, *, softcap=0.0, loss=None, lse=None, workspace=N
     st = lib().lm_linear_ce_fwd(n, d, v, softcap, _p(h), sh, _p(w), _p(target), _p(loss), _p(lse), _p(workspace),
                                 _nbytes(workspace), _stream(None))
     _check(st, "lm_linear_ce_fwd")
+    _written(*given)
     return loss, lse
 
 
@@ -306,6 +313,7 @@ def linear_ce_bwd(h, w, target, lse, dloss, dlse=None, *, softcap=0.0, grad_dtyp
         _want(t, name, _F32, target.shape, optional=name == "dlse")
         _dense(t, name)
     _code(grad_dtype)
+    given = (dh, dw)
     if dh is None:
         dh = torch.empty(h.shape, dtype=grad_dtype, device=dev)
     if dw is None:
@@ -318,6 +326,7 @@ def linear_ce_bwd(h, w, target, lse, dloss, dlse=None, *, softcap=0.0, grad_dtyp
     st = lib().lm_linear_ce_bwd(n, d, v, softcap, _p(h), sh, _p(w), _p(target), _p(lse), _p(dloss), _p(dlse), _p(dh),
                                 _p(dw), _code(dh.dtype), _p(workspace), _nbytes(workspace), _stream(None))
     _check(st, "lm_linear_ce_bwd")
+    _written(*given)
     return dict(dh=dh, dw=dw)
 
 
@@ -387,6 +396,7 @@ def adamw_step(params, grads, m, v, *, step, lr, betas=(0.9, 0.999), eps=1e-8, w
                              (ctypes.c_double * count)(*decay), lr, betas[0], betas[1], eps, int(step),
                              _stream(None))
     _check(st, "lm_adamw_step")
+    _written(*params)
 
 
 def adamw_state(p, bits=32):
