@@ -104,8 +104,8 @@ scan_status lm_linear_ce_fwd(int64_t n, int d, int64_t v, double softcap, const 
  * time:
  *   dz = (exp(z - lse) (dloss + dlse) - onehot(y) dloss) (1 - tanh^2),
  *   dh = dz w,  dw = dz^T h,
- * with dz rounded to BF16 for the two products.  dh [n, d] and dw [v, d] are of
- * grad_dtype, dense.
+ * with dz rounded to BF16 for the two products, also where grad_dtype is FP32 (a
+ * term is off by up to 2^-8 of itself).  dh [n, d] and dw [v, d] are of grad_dtype, dense.
  *   workspace  lm_linear_ce_workspace_bytes(n, d, v, 1) bytes */
 scan_status lm_linear_ce_bwd(int64_t n, int d, int64_t v, double softcap, const void* h, int64_t h_stride,
                              const void* w, const int64_t* target, const float* lse, const float* dloss,

@@ -225,5 +225,6 @@ class LinearCe(torch.autograd.Function):
 
 def linear_ce(h, w, target, *, softcap=0.0):
     """Token-wise cross entropy of the logits h w^T (capped where softcap > 0),
-    which are not kept; returns (loss, lse).  Negative targets do not count."""
+    which are not kept; returns (loss, lse).  Negative targets do not count.
+    The backward rounds the logits' cotangent to BF16 for its two products."""
     return LinearCe.apply(h, w, target, softcap)

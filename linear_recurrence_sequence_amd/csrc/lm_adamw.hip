@@ -14,8 +14,8 @@
 // 8-bit moments, 28 with FP32 weights and moments.  A lane holds 4 consecutive
 // elements, so a wave's 64 lanes hold exactly one block and its maximum is one
 // reduction over the wave; a wave requests 4 blocks before it uses the first.
-// 0.42 G weights with a BF16 copy and 8-bit moments take 1172 us, 5.75 TB/s; 58 M with
-// 32-bit ones 277 us, 5.97 TB/s (a large copy: 4.7 to 4.9 TB/s).
+// 0.42 G weights with a BF16 copy and 8-bit moments take 1175 us, 5.7 TB/s; 58 M with
+// 32-bit ones 277 us, 6.0 TB/s (a large copy: 4.7 to 4.9 TB/s).
 #include <float.h>
 
 #include "lm.hpp"

@@ -15,8 +15,8 @@
 //   dh += dz w_chunk (FP32 sums kept over the chunks),  dw_chunk = dz^T h.
 //
 // Bound by the matrix cores for many tokens (2 n d v flops forward, 6 n d v
-// backward): 8192 x 2048 x 128000 forward + backward 12.8 ms, 1.35 PFLOP/s, where
-// four library products of the shape alone take 13.2; by reading w, and writing
+// backward): 8192 x 2048 x 128000 forward + backward 12.9 ms, 1.33 PFLOP/s, where
+// four library products of the shape alone take 13.1; by reading w, and writing
 // dw, for few: 16 x 1024 x 32000 forward 12.5 us, 5.2 TB/s, and a second launch.
 #include "lm_ce_plan.hpp"
 #include "lm_gemm.hpp"
@@ -202,7 +202,9 @@ __device__ __forceinline__ void pack_row(const CeArgs& a, int from, int to) {
     u32x4_t* o = reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(a.packed) + (int64_t)to * a.d);
     for (int i = threadIdx.x & 63; i < a.d / 8; i += 64) o[i] = p[i];
 }
-constexpr int LIST_PACKS = 1024;  // tokens up to which the listing launch packs
+// Tokens up to which the listing launch packs.  Backward of 1024 tokens x 1024 x 1000 43.0 us, 48.3 with a packing launch; of 512 38.1 and 40.7.
+// Every workgroup walks all tokens for its list, so that the gain ends: of 2048 50.4 and 52.5, of 8192 126 and 128.
+constexpr int LIST_PACKS = 1024;
 
 // Lists the tokens that take part, those with a weight, in their order; the
 // products run over these alone, so prompt and padding tokens cost nothing and
@@ -653,6 +655,8 @@ hipError_t launch_ce_bwd(const CeArgs& args, hipStream_t s) {
         }
     }
     const int64_t quads = (int64_t)a.n * a.d / 4;
+    // Eight lanes a sum against one: of 125 ranges (16 x 512 x 32000) the backward takes 36.3 us against 39.8, of 63 (16 x 1024 x 32000)
+    // 49.4 against 51.5; of 12 (600 x 1024 x 32000) 173.9 against 171.1, of 8 (2048 x 1024 x 32000) 389 against 384; between them either way, by 1%.
     if (pl.splits >= 16) LRS_LAUNCH(K_LM_CE_JOIN, ce_dh_join_kernel<8>, dim3((unsigned)ceil_div(quads, 32)), dim3(256), 0, s, a, pl.splits);
     else LRS_LAUNCH(K_LM_CE_JOIN, ce_dh_join_kernel<1>, dim3((unsigned)ceil_div(quads, 256)), dim3(256), 0, s, a, pl.splits);
     return hipGetLastError();

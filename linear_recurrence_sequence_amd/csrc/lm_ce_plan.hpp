@@ -15,7 +15,10 @@ constexpr int CE_STEP = 64;  // reduction indices of a tile product's step
 enum Shape { LARGE, SMALL, FEW };
 constexpr int kBM[3] = {256, 128, 64}, kBN[3] = {256, 128, 32};
 
-constexpr int kFew = 256;  // tokens up to which the backward goes by the bytes of w and dw
+// Tokens up to which the backward goes by the bytes of w and dw: dz lies [entries, tokens], and dw is streamed.  By that and by the
+// form for many tokens, 2048 x 128000: 33 tokens 412 and 471 us, 128 466 and 523, 129 595 and 564, 192 598 and 610, 256 607 and 648;
+// 1024 x 32000: 64 60 and 70, 129 90 and 98, 256 98 and 104.  Small heads gain nothing from it: 512 x 4000, 256 tokens, 38 and 33.
+constexpr int kFew = 256;
 constexpr int64_t kMostDz = (int64_t)128 << 20;  // elements of dz held at once
 
 // Time of a product of p x q results over k, in microseconds: rounds of

@@ -19,8 +19,10 @@
 // every load of a wave covers whole lines.  With W = 1 a workgroup holds four
 // rows (eight or 16 of up to 128 or 64 columns, on half or a quarter of a wave) and needs no barrier.  Workgroups walk over rows with the weights in
 // registers, and the backward keeps its column sums there until the end.
-// 32768 x 2560, FP32 stream and BF16 branch with a gate: forward 221 us, 5.3 TB/s;
-// backward 322 us, 5.7 TB/s (a large copy runs at 4.7 TB/s).
+// 32768 x 2560, FP32 stream and BF16 branch with a gate, call after call: forward 217 us, 5.4 TB/s;
+// backward 312 us with the column sums, 5.9 TB/s (a large copy runs at 4.8 TB/s; traced one by one the two take 222 and 342 us).
+// Above 8192 columns the backward's four groups a lane do not fit the 128 registers of a 16-wave workgroup: 65 to 199 spill,
+// and 4096 x 16384 BF16 takes 445 us, 2.4 TB/s (878 where the width is odd); the forward does not spill (147 us, 4.6 TB/s).
 #include "lm.hpp"
 
 namespace lrs {
@@ -377,13 +379,16 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* part, in
     }
 }
 
-// Waves of a row: NV groups of 256 columns a wave.  Few rows leave the chip
-// idle however they are spread, so they take one group a lane (the shortest
-// chain of loads and sums).  Of many rows, those up to 1024 columns are one
-// wave's: four rows are then in flight in a workgroup and no barrier stands
-// between them (backward of 4096 x 1024 bf16: 23 us, 31 us with two waves a row;
-// of 32768 x 1024: 103 us, 112 us), up to 128 and 64 columns half a wave's or a
-// quarter's (backward of 32768 x 64 bf16: 15 us, 44 us with a wave a row).  Wider ones take two groups a wave, four above 8192
+// Waves of a row: NV groups of 256 columns a wave.  Times are of BF16 calls, column sums included; one plan serves both
+// directions, whose rows lie alike.
+//   Few rows leave the chip idle however they are spread, so they take one group a lane (the shortest
+// chain of loads and sums).  The backward of 512 x 4096: 19.9 us, 24.5 with two groups; of 512 x 2048 16.5 and 17.0; of 1024 x 1024
+// 13.6 and 12.5, of 1024 x 512 13.8 and 11.8 (1024 x 2048 would still gain, 19.3 and 20.5).  The forward of so few is a launch either way, 6 us.
+//   Of many rows, those up to 1024 columns are one wave's: four rows are then in flight in a workgroup and no barrier stands
+// between them.  Backward of 4096 x 1024 22.8 us, 29.0 with two waves a row; of 32768 x 1024 102.6 and 111.3.  Forward of the two 10.9 and 9.9,
+// 63.0 and 62.8.  Up to 128 and 64 columns half a wave's or a quarter's: 32768 x 64 backward 14 us, 32 with a wave a row, forward 7.6 and 15.1;
+// 32768 x 128 backward 21.7 and 28.4, forward 12.4 and 16.7.
+//   Wider ones take two groups a wave, four above 8192
 // columns, where a row would not fit the 16 waves of a workgroup.
 struct Plan {
     int nv, waves, lanes;  // lanes of a row where it is no more than a wave's, else 0
@@ -439,18 +444,21 @@ void launch_any(const NormArgs& a, int stream_f32, int branch_f32, int blocks, h
 }  // namespace
 
 // Workgroups that walk over the rows.  Each writes its column sums, and HBM
-// serves few long streams better than many: with 5 waves a row (32768 x 2560)
-// 512 workgroups take 322 us, 256 478, 768 380, 1024 410; with 16 (4096 x 8192)
-// 256 take 153 us, 512 165; with 2 (8192 x 1024) 1024 took 47 us, 512 55; narrow rows
-// that are less than a wave's work wait for memory more (32768 x 256: 1024 take 35 us, 512 41).
+// serves few long streams better than many.  Half of them, these, 1.5 and 2 times as many take, in BF16 but for the first:
+//   5 waves a row   32768 x 2560, FP32 stream   484, 312, 378, 410 us
+//   16              4096 x 8192                 186, 130, 157, 142
+//   3               8192 x 1536                  59,  52,  62,  61
+//   one             32768 x 1024                126, 103, 115, 109
+//   one, narrow     32768 x 256                  39,  33,  37,  43
+//   half, a quarter 32768 x 128, x 64            23,  21,  24,  28;  19, 14, 15, 16
 int lm_norm_bwd_blocks(int64_t rows, int d) {
     const Plan p = plan(rows, d);
     const int most = p.lanes ? (d > 64 && d <= 256 ? 1024 : 512) : p.waves > 8 ? 256 : p.waves >= 4 ? 512 : 1024;
     return (int)std::min<int64_t>(ceil_div(rows, p.lanes ? 256 / p.lanes : 1), most);
 }
 
-// The forward keeps nothing between rows; only the widest rows gain from
-// fewer workgroups (4096 x 8192: 768 take 87 us, 4096 100; 32768 x 2560: 221 us either way).
+// The forward keeps nothing between rows, and its count matters little: with more than 8 waves a row 768 workgroups take
+// 70 us for 4096 x 8192, 4096 72; with fewer waves 4096 take 82 us for 32768 x 1280 and 217 for 32768 x 2560 with an FP32 stream, 768 102 and 213.
 hipError_t launch_norm_fwd(const NormArgs& a, int stream_f32, int branch_f32, hipStream_t s) {
     const Plan p = plan(a.rows, a.d);
     launch_any<false>(a, stream_f32, branch_f32,

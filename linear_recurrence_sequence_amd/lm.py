@@ -297,7 +297,11 @@ def linear_ce_bwd(h, w, target, lse, dloss, dlse=None, *, softcap=0.0, grad_dtyp
                   workspace=None, stream=None):
     """Gradients of linear_ce_fwd for the cotangents dloss and dlse (FP32, as
     the target; dlse None = 0), from its lse.  Returns dict(dh, dw) of
-    grad_dtype."""
+    grad_dtype.
+
+    The cotangent of the logits, dz, is rounded to BF16 for the two products, whose operands are BF16 and whose sums
+    are FP32, whatever grad_dtype is: a term of dh and dw is off by up to 2^-8 of itself, and FP32 gradients save the
+    last rounding alone.  BF16 gradients of 2048 tokens x 1024 x 32000 are 0.0019 of their size from 64 bits, with dz in FP32 0.0017."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return linear_ce_bwd(h, w, target, lse, dloss, dlse, softcap=softcap, grad_dtype=grad_dtype, dh=dh, dw=dw, workspace=workspace)
