@@ -45,6 +45,7 @@ enum { LM_GATE_NONE = 0, LM_GATE_SIGMOID = 1, LM_GATE_SILU = 2 };
  *   y     [rows, d] of branch_dtype; gate the same or NULL
  *   w_post, scale  f32 [d], both or neither;  w_pre  f32 [d]
  *   r     [rows, d] of stream_dtype, dense; may be x itself where x is dense
+ *         (the backward reads x as it was before)
  *   n     [rows, d] of branch_dtype, dense
  *   stats f32 [rows, 2]: (rs1, rs2) for the backward (rs1 = 1 in the plain form)
  * rows >= 0 (0: nothing to do), 1 <= d <= LM_NORM_MAX_D. */

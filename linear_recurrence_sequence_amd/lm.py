@@ -157,7 +157,7 @@ def block_norm_fwd(x, y, gate, w_post, scale, w_pre, *, eps=1e-6, gate_act="none
     x [..., d] BF16 or FP32 (the stream), y and gate [..., d] BF16 or FP32 (the
     branch); rows may lie apart (views of a wider projection).  gate_act is
     "none" (gate None), "sigmoid" or "silu"; weights are FP32 [d].  r may be x
-    itself.  Returns (r [stream dtype], n [branch dtype], stats f32 [rows, 2])."""
+    itself (not before a backward, which reads x as it was).  Returns (r [stream dtype], n [branch dtype], stats f32 [rows, 2])."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return block_norm_fwd(x, y, gate, w_post, scale, w_pre, eps=eps, gate_act=gate_act, r=r, n=n, stats=stats)
