@@ -2,7 +2,8 @@
  * lm_ops.h -- C ABI of the language-model operators that stand around the
  * recurrent mixers of samu_scan.h on MI355X (gfx950): the norms before and
  * after a block with its gate and residual scale, the softmax cross entropy of
- * a linear head without the logits, and the AdamW step over many tensors.
+ * a linear head without the logits, the AdamW step over many tensors, and the
+ * embedding lookup.
  *
  * Conventions are those of samu_scan.h (device pointers, asynchronous on
  * `stream`, all arguments validated before the first enqueue, no allocation,
@@ -10,7 +11,7 @@
  * scan_status and scan_last_error()) with these differences:
  *   - activations are rows with a stride in elements between them (columns
  *     dense), so parts of a wider projection are taken as they lie;
- *   - norm and AdamW pointers need only the alignment of their element type.
+ *   - norm, AdamW and embedding pointers need only the alignment of their element type.
  */
 #ifndef LM_OPS_H
 #define LM_OPS_H
@@ -135,6 +136,29 @@ scan_status lm_adamw_step(int count, int param_dtype, int grad_dtype, int state_
                           float* const* master, float* const* m_scale, float* const* v_scale,
                           const int64_t* n, const double* decay,
                           double lr, double beta1, double beta2, double eps, int64_t step, void* stream);
+
+/* ======================================================================
+ * Embedding lookup: out_t = scale w[tok_t], for tokens int64 [n] and the
+ * vocabulary's rows w [v, d].  A negative token is padding: its row of out is
+ * zero, and it has no gradient.  A token >= v: its row is NaN, without one either.
+ * Products are FP32, out is rounded once (where it is BF16).
+ * 1 <= d <= 2^24, v >= 1, 0 <= n < 2^27, v + n / 16 < 2^26 - 32, n ceil(d / 4) < 2^32 - 256.
+ * ====================================================================== */
+
+/* Forward.  w [v, d] of w_dtype and out [n, d] of out_dtype, dense. */
+scan_status lm_embed_fwd(int64_t n, int d, int64_t v, int w_dtype, int out_dtype, double scale, const int64_t* tokens,
+                         const void* w, void* out, void* stream);
+
+/* Backward for the cotangent dout [n, d] of out_dtype, row stride dout_stride:
+ *   dw_v = scale sum_{t: tok_t = v} dout_t,
+ * summed in FP32 in an order that the tokens alone decide, rounded once; dw [v, d] of
+ * grad_dtype, dense.  Rows without tokens are zero.  accumulate: the sums are added to what dw
+ * holds (of a head tied to the embedding), in FP32 before the rounding, and rows without tokens are left as they are.
+ *   workspace  lm_embed_bwd_workspace_bytes(n, d, v) bytes */
+size_t lm_embed_bwd_workspace_bytes(int64_t n, int d, int64_t v);
+scan_status lm_embed_bwd(int64_t n, int d, int64_t v, int out_dtype, int grad_dtype, double scale,
+                         const int64_t* tokens, const void* dout, int64_t dout_stride, int accumulate, void* dw,
+                         void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

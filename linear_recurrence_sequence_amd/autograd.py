@@ -1,4 +1,4 @@
-"""The scans and the gate projections as differentiable torch operations.
+"""The scans, the projections and the language-model operators as differentiable torch operations.
 
 Each forward calls the library's forward entry point and keeps its saved
 record (a uint8 tensor) for the backward; each backward calls the adjoint
@@ -10,7 +10,7 @@ library.  The streams (x_sel, b; x, l^x, l^a) must be BF16, the library's
 input format: a tensor of another dtype is refused rather than converted."""
 import torch
 
-from . import lm, scan
+from . import lm, scan, ssm
 
 
 def _need_bf16(**tensors):
@@ -228,3 +228,81 @@ def linear_ce(h, w, target, *, softcap=0.0):
     which are not kept; returns (loss, lse).  Negative targets do not count.
     The backward rounds the logits' cotangent to BF16 for its two products."""
     return LinearCe.apply(h, w, target, softcap)
+
+
+class Embed(torch.autograd.Function):
+    """Embedding lookup: w -> out, as lm.embed_fwd.  A second derivative raises."""
+
+    @staticmethod
+    def forward(ctx, tokens, w, scale, out_dtype):
+        ctx.save_for_backward(tokens)
+        ctx.v, ctx.scale, ctx.dtype = w.shape[0], scale, w.dtype
+        return lm.embed_fwd(tokens, w, scale=scale, out_dtype=out_dtype)
+
+    @staticmethod
+    def backward(ctx, dout):
+        tokens, = ctx.saved_tensors
+        dw = lm.embed_bwd(tokens, dout.contiguous(), ctx.v, scale=ctx.scale, grad_dtype=ctx.dtype)
+        return (None, *_once("embed", (dw,), dout), None, None)
+
+
+def embed(tokens, w, *, scale=1.0, out_dtype=None):
+    """Rows of an embedding, scale * w[tokens]; a negative token's row is zero.
+    The gradient is dense, summed in a fixed order."""
+    return Embed.apply(tokens, w, scale, out_dtype)
+
+
+class SsmScan(torch.autograd.Function):
+    """Selective scan: (u, dt, a, b, c, d, z, dt_bias, h0) -> (y, h_final), as
+    ssm.ssm_scan_fwd.  A second derivative raises."""
+
+    @staticmethod
+    def forward(ctx, u, dt, a, b, c, d, z, dt_bias, h0, softplus, reset, lengths):
+        y, h, saved = ssm.ssm_scan_fwd(u, dt, a, b, c, d, z, dt_bias, h0, softplus=softplus, reset=reset, lengths=lengths,
+                                       want_saved=any(ctx.needs_input_grad))
+        ctx.save_for_backward(u, dt, a, b, c, d, z, dt_bias, reset, lengths, saved)
+        ctx.softplus, ctx.has_h0 = softplus, h0 is not None
+        ctx.set_materialize_grads(False)
+        return y, h
+
+    @staticmethod
+    def backward(ctx, dy, dh):
+        u, dt, a, b, c, d, z, dt_bias, reset, lengths, saved = ctx.saved_tensors
+        # expanded cotangents (of a sum) have no rows to read: lay them out
+        dy = torch.zeros_like(u, memory_format=torch.contiguous_format) if dy is None else dy.contiguous()
+        dh = None if dh is None else dh.contiguous()
+        g = ssm.ssm_scan_bwd(u, dt, a, b, c, d, z, dt_bias, saved, dy, dh, softplus=ctx.softplus, reset=reset, lengths=lengths, want_dh0=ctx.has_h0)
+        grads = tuple(g.get(k) for k in ("du", "ddt", "da", "db", "dc", "dd", "dz", "ddt_bias", "dh0"))
+        return (*_once("ssm_scan", grads, u, dt, a, b, c, d, z, dt_bias, dy, dh), None, None, None)
+
+
+def ssm_scan(u, dt, a, b, c, d=None, z=None, dt_bias=None, h0=None, *, softplus=True, reset=None, lengths=None):
+    """Selective state space scan with its gate; returns (y, h_final)."""
+    return SsmScan.apply(u, dt, a, b, c, d, z, dt_bias, h0, softplus, reset, lengths)
+
+
+class CausalConv(torch.autograd.Function):
+    """Short causal convolution: (x, w, bias, state) -> (y, state_out), as
+    ssm.causal_conv_fwd.  A second derivative raises."""
+
+    @staticmethod
+    def forward(ctx, x, w, bias, state, act, reset, lengths):
+        y, last = ssm.causal_conv_fwd(x, w, bias, act=act, state=state, reset=reset, lengths=lengths)
+        ctx.save_for_backward(x, w, bias, state, reset, lengths)
+        ctx.act = act
+        ctx.set_materialize_grads(False)
+        return y, last
+
+    @staticmethod
+    def backward(ctx, dy, dlast):
+        x, w, bias, state, reset, lengths = ctx.saved_tensors
+        dy = torch.zeros_like(x, memory_format=torch.contiguous_format) if dy is None else dy.contiguous()
+        dlast = None if dlast is None else dlast.contiguous()
+        g = ssm.causal_conv_bwd(x, w, bias, dy, dlast, act=ctx.act, state=state, reset=reset, lengths=lengths)
+        grads = tuple(g.get(k) for k in ("dx", "dw", "dbias", "dstate"))
+        return (*_once("causal_conv", grads, x, w, bias, state, dy, dlast), None, None, None)
+
+
+def causal_conv(x, w, bias=None, state=None, *, act="silu", reset=None, lengths=None):
+    """Short causal convolution of each channel over time; returns (y, state_out)."""
+    return CausalConv.apply(x, w, bias, state, act, reset, lengths)

@@ -22,7 +22,7 @@ BIND = os.path.join(HERE, "_lm_bind.so")
 ARCH = "gfx950"
 
 SOURCES = ["capi.cpp", "prefix.hip", "samu_fwd.hip", "samu_bwd.hip", "samu_decode.hip", "rglru.hip", "baseline.hip", "gate_proj.hip", "noalloc.hip",
-           "lm_capi.cpp", "lm_norm.hip", "lm_adamw.hip", "lm_ce.hip"]
+           "lm_capi.cpp", "lm_norm.hip", "lm_adamw.hip", "lm_ce.hip", "lm_embed.hip", "ssm_capi.cpp", "ssm_fwd.hip", "ssm_bwd.hip", "ssm_conv.hip"]
 
 CXXFLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

@@ -61,7 +61,9 @@ static const char* const kKernelNames[K_NUM_KERNELS] = {
     "baseline_sequential", "baseline_associative", "gate_projection", "gate_projection_dx",
     "gate_projection_dw", "gate_projection_reduce", "samu_forward_scan", "samu_backward_scan", "clear",
     "gate_projection_adjoint", "rglru_forward_scan", "rglru_backward_scan", "block_norm", "block_norm_backward",
-    "block_norm_reduce", "adamw", "linear_ce_stats", "linear_ce_join", "linear_ce_list", "linear_ce_dz", "linear_ce_dh", "linear_ce_dw"};
+    "block_norm_reduce", "adamw", "linear_ce_stats", "linear_ce_join", "linear_ce_list", "linear_ce_dz", "linear_ce_dh", "linear_ce_dw",
+    "embed", "embed_sort", "embed_grad", "embed_join", "ssm_summary", "ssm_scan", "ssm_step", "ssm_reverse_summary", "ssm_backward",
+    "ssm_join", "causal_conv", "causal_conv_step", "causal_conv_backward", "causal_conv_join"};
 
 const char* kernel_name(int id) { return (id >= 0 && id < K_NUM_KERNELS) ? kKernelNames[id] : "?"; }
 

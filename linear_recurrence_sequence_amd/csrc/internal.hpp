@@ -53,6 +53,20 @@ enum KernelId {
     K_LM_CE_DZ,
     K_LM_CE_DH,
     K_LM_CE_DW,
+    K_LM_EMBED,
+    K_LM_EMBED_SORT,
+    K_LM_EMBED_GRAD,
+    K_LM_EMBED_JOIN,
+    K_SSM_SUMMARY,
+    K_SSM_SCAN,
+    K_SSM_STEP,
+    K_SSM_REV,
+    K_SSM_BWD,
+    K_SSM_JOIN,
+    K_CONV,
+    K_CONV_STEP,
+    K_CONV_BWD,
+    K_CONV_JOIN,
     K_NUM_KERNELS
 };
 

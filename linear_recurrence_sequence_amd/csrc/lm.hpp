@@ -1,5 +1,5 @@
 // lm.hpp -- declarations and device helpers shared by the language-model
-// operators (block norms, linear cross entropy, AdamW).
+// operators (block norms, linear cross entropy, AdamW, embedding lookup).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -76,6 +76,39 @@ struct Quad<float> {
     }
 };
 
+// Rows in groups of four elements.  Where
+// the width is no multiple of 4 (TAIL) the group that the row ends in is loaded as the
+// row's last four elements and put in place by take(), so that no load stands in a
+// branch of its own (each would be waited for there).
+template <class T, bool TAIL>
+__device__ __forceinline__ Quad<T> row_load(const T* row, int col, int d) {
+    if (TAIL) {
+        if (d < 4) return col < d ? Quad<T>::load_some(row, d) : Quad<T>::zero();
+        return Quad<T>::load(row + (col + 4 <= d ? col : d - 4));
+    }
+    if (col + 4 <= d) return Quad<T>::load(row + col);
+    return Quad<T>::zero();
+}
+template <bool TAIL, class T>
+__device__ __forceinline__ void take(const Quad<T>& q, int col, int d, float* f) {
+    q.get(f);
+    if (TAIL) {
+        const int n = d < 4 && col < d ? 4 : d - col;  // this lane's elements, 4 or more: all
+        if (n < 4) {
+            const float a = f[1], b = f[2], c = f[3];
+            f[0] = n == 3 ? a : n == 2 ? b : n == 1 ? c : 0.0f;
+            f[1] = n == 3 ? b : n == 2 ? c : 0.0f;
+            f[2] = n == 3 ? c : 0.0f;
+            f[3] = 0.0f;
+        }
+    }
+}
+template <class T, bool TAIL>
+__device__ __forceinline__ void row_store(T* row, int col, int d, const float* f) {
+    if (col + 4 <= d) Quad<T>::store(row + col, f);
+    else if (TAIL && col < d) Quad<T>::store_some(row + col, f, d - col);
+}
+
 // ---------------------------------------------------------- block norms ---
 struct NormArgs {
     int64_t rows;
@@ -146,5 +179,26 @@ struct CeArgs {
 };
 hipError_t launch_ce_fwd(const CeArgs& a, hipStream_t s);
 hipError_t launch_ce_bwd(const CeArgs& a, hipStream_t s);
+
+// ------------------------------------------------------ embedding lookup ---
+constexpr int EMBED_ROWS = 512;   // rows of the vocabulary that a sorting workgroup takes
+constexpr int EMBED_RUN = 32;     // tokens that one wave adds up for a row
+struct EmbedArgs {
+    int64_t n, v;                 // tokens, rows of the vocabulary
+    int d;
+    float scale;
+    const int64_t* tokens;        // [n]; negative: padding
+    const void* w;                // [v, d]
+    void* out;                    // [n, d]
+    // backward
+    const void* dout;             // [n, d], row stride dout_stride
+    int64_t dout_stride;
+    void* dw;                     // [v, d]
+    int add;                      // to what dw holds
+    int *start, *order;           // [v + 1], [n]: where each row's tokens begin in the order
+    float* part;                  // [ceil(n / EMBED_RUN), 2, d]: what a run holds of the row that it begins and ends in
+};
+hipError_t launch_embed_fwd(const EmbedArgs& a, bool w_f32, bool out_f32, hipStream_t s);
+hipError_t launch_embed_bwd(const EmbedArgs& a, bool out_f32, bool grad_f32, hipStream_t s);
 
 }  // namespace lrs

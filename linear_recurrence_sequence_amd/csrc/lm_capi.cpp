@@ -4,64 +4,16 @@
 
 #include <algorithm>
 #include <cmath>
-#include <initializer_list>
 #include <string>
 #include <vector>
 
+#include "capi_check.hpp"
 #include "lm.hpp"
 #include "lm_ce_plan.hpp"
 #include "lm_ops.h"
 
 namespace lrs {
 namespace {
-
-scan_status fail(scan_status st, const std::string& msg) { return (scan_status)set_last_error(st, msg.c_str()); }
-
-// A tensor argument: `n` bytes from p, aligned to `align` bytes.
-struct Arg {
-    const void* p;
-    size_t n, align;
-    const char* name;
-};
-
-scan_status check_args(std::initializer_list<Arg> req, std::initializer_list<Arg> opt) {
-    for (const Arg& a : req)
-        if (!a.p) return fail(SCAN_ERR_NULL, std::string(a.name) + " is NULL");
-    for (const auto* list : {&req, &opt})
-        for (const Arg& a : *list)
-            if (a.p && ((uintptr_t)a.p & (a.align - 1)))
-                return fail(SCAN_ERR_ALIGN, std::string(a.name) + " is not " + std::to_string(a.align) + "-byte aligned");
-    return SCAN_OK;
-}
-
-bool overlap(const Arg& a, const Arg& b) {
-    if (!a.p || !b.p || !a.n || !b.n) return false;
-    const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
-    return a0 < b0 + b.n && b0 < a0 + a.n;
-}
-
-// outputs must not overlap inputs nor each other
-scan_status check_alias(std::initializer_list<Arg> ins, std::initializer_list<Arg> outs) {
-    for (auto o = outs.begin(); o != outs.end(); ++o) {
-        for (const Arg& i : ins)
-            if (overlap(*o, i)) return fail(SCAN_ERR_ALIAS, std::string(o->name) + " overlaps " + i.name);
-        for (auto q = o + 1; q != outs.end(); ++q)
-            if (overlap(*o, *q)) return fail(SCAN_ERR_ALIAS, std::string(o->name) + " overlaps " + q->name);
-    }
-    return SCAN_OK;
-}
-
-scan_status device_status(hipError_t e, const char* where) {
-    if (e == hipSuccess) return SCAN_OK;
-    return fail(SCAN_ERR_DEVICE, std::string(where) + ": " + hipGetErrorString(e));
-}
-
-bool dtype_ok(int t) { return t == SCAN_BF16 || t == SCAN_F32; }
-size_t dtype_size(int t) { return t == SCAN_F32 ? 4 : 2; }
-// bytes from the first to the last element of `rows` rows
-size_t span(int64_t rows, int64_t stride, int d, size_t size) {
-    return rows > 0 ? ((size_t)(rows - 1) * (size_t)stride + (size_t)d) * size : 0;
-}
 
 constexpr int64_t kMaxRows = (int64_t)1 << 40;
 // a tile's 256 rows, or 64 steps, stay inside the 31-bit offsets of a buffer descriptor
@@ -125,6 +77,31 @@ scan_status ce_check(const char* fn, int64_t n, int d, int64_t v, double cap, in
     if (n > 0 && (h_stride % 8 != 0 || h_stride < 0 || h_stride > kMaxCeStride))
         return fail(SCAN_ERR_SHAPE, std::string(fn) + ": the rows of h must lie a multiple of 8 elements apart");
     return SCAN_OK;
+}
+
+// Launches of a thread for four columns of a token, 64 for a row of the vocabulary, 32 for a token.
+bool embed_shape(int64_t n, int d, int64_t v) {
+    return n >= 0 && d >= 1 && v >= 1 && n <= (MOST_THREADS - 1024) / 32 && v <= (MOST_THREADS - 1024) / 64 - n / 16 - 8 && d <= (1 << 24) &&
+           (__int128)n * ceil_div(d, 4) <= MOST_THREADS - 256;
+}
+scan_status embed_refuse(const char* fn, int64_t n, int d, int64_t v) {
+    return fail(SCAN_ERR_SHAPE, std::string(fn) + ": unsupported shape n=" + std::to_string(n) + " d=" + std::to_string(d) + " v=" +
+                                    std::to_string(v) + " (need 1 <= d <= 2^24, v >= 1, n < 2^27, v + n / 16 < 2^26 - 32, n ceil(d / 4) < 2^32 - 256)");
+}
+
+// The gradient's buffers inside the caller's workspace (base NULL: sizes only).
+size_t embed_layout(int64_t n, int d, int64_t v, void* base, EmbedArgs* a) {
+    char* p = static_cast<char*>(base);
+    size_t off = 0;
+    const auto take = [&](size_t bytes) {
+        void* at = p ? p + off : nullptr;
+        off += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    a->start = static_cast<int*>(take((size_t)(v + 1) * 4));
+    a->order = static_cast<int*>(take((size_t)n * 4));
+    a->part = static_cast<float*>(take((size_t)ceil_div(n, EMBED_RUN) * 2 * d * 4));
+    return std::max<size_t>(off, 256);
 }
 
 }  // namespace
@@ -384,6 +361,55 @@ scan_status lm_adamw_step(int count, int param_dtype, int grad_dtype, int state_
         }
     }
     return device_status(flush(), "adamw");
+}
+
+// --------------------------------------------------- embedding lookup ---
+size_t lm_embed_bwd_workspace_bytes(int64_t n, int d, int64_t v) {
+    if (!embed_shape(n, d, v)) return 0;
+    EmbedArgs a{};
+    return embed_layout(n, d, v, nullptr, &a);
+}
+
+scan_status lm_embed_fwd(int64_t n, int d, int64_t v, int w_dtype, int out_dtype, double scale, const int64_t* tokens, const void* w,
+                         void* out, void* stream) {
+    if (!embed_shape(n, d, v)) return embed_refuse("lm_embed_fwd", n, d, v);
+    if (!dtype_ok(w_dtype) || !dtype_ok(out_dtype)) return fail(SCAN_ERR_SHAPE, "lm_embed_fwd: dtypes must be SCAN_BF16 or SCAN_F32");
+    if (!std::isfinite((float)scale)) return fail(SCAN_ERR_SHAPE, "lm_embed_fwd: scale must be finite");
+    if (n == 0) return SCAN_OK;
+    const size_t ws = dtype_size(w_dtype), os = dtype_size(out_dtype);
+    const Arg at{tokens, (size_t)n * 8, 8, "tokens"}, aw{w, (size_t)v * d * ws, ws, "w"}, ao{out, (size_t)n * d * os, os, "out"};
+    scan_status st = check_args({at, aw, ao}, {});
+    if (st == SCAN_OK) st = check_alias({at, aw}, {ao});
+    if (st != SCAN_OK) return st;
+    EmbedArgs a{};
+    a.n = n, a.v = v, a.d = d, a.scale = (float)scale;
+    a.tokens = tokens, a.w = w, a.out = out;
+    return device_status(launch_embed_fwd(a, w_dtype == SCAN_F32, out_dtype == SCAN_F32, (hipStream_t)stream), "embedding");
+}
+
+scan_status lm_embed_bwd(int64_t n, int d, int64_t v, int out_dtype, int grad_dtype, double scale, const int64_t* tokens,
+                         const void* dout, int64_t dout_stride, int accumulate, void* dw, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+    if (!embed_shape(n, d, v)) return embed_refuse("lm_embed_bwd", n, d, v);
+    if (!dtype_ok(out_dtype) || !dtype_ok(grad_dtype)) return fail(SCAN_ERR_SHAPE, "lm_embed_bwd: dtypes must be SCAN_BF16 or SCAN_F32");
+    if (!std::isfinite((float)scale)) return fail(SCAN_ERR_SHAPE, "lm_embed_bwd: scale must be finite");
+    if (n > 0 && (dout_stride < 0 || dout_stride > kMaxRows)) return fail(SCAN_ERR_SHAPE, "lm_embed_bwd: row strides must not be negative");
+    const size_t os = dtype_size(out_dtype), gs = dtype_size(grad_dtype);
+    EmbedArgs a{};
+    const size_t need = embed_layout(n, d, v, nullptr, &a);
+    const Arg at{tokens, (size_t)n * 8, 8, "tokens"}, ao{dout, span(n, dout_stride, d, os), os, "dout"}, aw{dw, (size_t)v * d * gs, gs, "dw"},
+        ws{workspace, need, 16, "workspace"};
+    scan_status st = n > 0 ? check_args({at, ao, aw, ws}, {}) : check_args({aw}, {});
+    if (st != SCAN_OK) return st;
+    if (n > 0 && workspace_bytes < need)
+        return fail(SCAN_ERR_WORKSPACE, "lm_embed_bwd: workspace_bytes " + std::to_string(workspace_bytes) + " < " + std::to_string(need));
+    if (n > 0) st = check_alias({at, ao}, {aw, ws});
+    if (st != SCAN_OK) return st;
+    if (n == 0 && accumulate) return SCAN_OK;
+    embed_layout(n, d, v, workspace, &a);
+    a.n = n, a.v = v, a.d = d, a.scale = (float)scale, a.add = accumulate != 0;
+    a.tokens = tokens, a.dout = dout, a.dout_stride = dout_stride, a.dw = dw;
+    return device_status(launch_embed_bwd(a, out_dtype == SCAN_F32, grad_dtype == SCAN_F32, (hipStream_t)stream), "embedding backward");
 }
 
 }  // extern "C"

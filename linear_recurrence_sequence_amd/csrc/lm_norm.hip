@@ -61,38 +61,6 @@ __device__ __forceinline__ float sigmoid(float g, float* rest) {
     return s;
 }
 
-// Which elements a lane holds: group c starts at column c * 4 T + 4 t.  Where
-// the width is no multiple of 4 (TAIL) the group that the row ends in is loaded as the
-// row's last four elements and put in place by take(), so that no load stands in a
-// branch of its own (each would be waited for there).
-template <class T, bool TAIL>
-__device__ __forceinline__ Quad<T> row_load(const T* row, int col, int d) {
-    if (TAIL) {
-        if (d < 4) return col < d ? Quad<T>::load_some(row, d) : Quad<T>::zero();
-        return Quad<T>::load(row + (col + 4 <= d ? col : d - 4));
-    }
-    if (col + 4 <= d) return Quad<T>::load(row + col);
-    return Quad<T>::zero();
-}
-template <bool TAIL, class T>
-__device__ __forceinline__ void take(const Quad<T>& q, int col, int d, float* f) {
-    q.get(f);
-    if (TAIL) {
-        const int n = d < 4 && col < d ? 4 : d - col;  // this lane's elements, 4 or more: all
-        if (n < 4) {
-            const float a = f[1], b = f[2], c = f[3];
-            f[0] = n == 3 ? a : n == 2 ? b : n == 1 ? c : 0.0f;
-            f[1] = n == 3 ? b : n == 2 ? c : 0.0f;
-            f[2] = n == 3 ? c : 0.0f;
-            f[3] = 0.0f;
-        }
-    }
-}
-template <class T, bool TAIL>
-__device__ __forceinline__ void row_store(T* row, int col, int d, const float* f) {
-    if (col + 4 <= d) Quad<T>::store(row + col, f);
-    else if (TAIL && col < d) Quad<T>::store_some(row + col, f, d - col);
-}
 template <bool TAIL>
 __device__ __forceinline__ void weight_load(const float* w, int col, int d, float missing, float* f) {
     if (w) {

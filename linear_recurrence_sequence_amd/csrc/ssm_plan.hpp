@@ -1,0 +1,68 @@
+// ssm_plan.hpp -- how the selective scan is spread over the chip.  Plain host
+// code, shared by the launches and the workspace sizes.
+#pragma once
+
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "ints.hpp"
+
+namespace lrs {
+
+constexpr int SSM_TOK = 16;       // tokens of a chunk: a state is kept before each
+constexpr int SSM_STATES = 4;     // states of a lane, for two channels
+constexpr int SSM_MOST_N = 64;
+
+// A wave takes 128 / ng channels and all states: its lanes are ng groups (of
+// SSM_STATES states each) of 64 / ng channel pairs.
+inline int ssm_state_groups(int n) {
+    int ng = 1;
+    while (ng * SSM_STATES < n) ng *= 2;
+    return ng;
+}
+
+struct SsmPlan {
+    int ng;               // state groups of a wave
+    int tiles;            // waves over the channels of one group of b and c
+    int waves;            // waves of a workgroup (in the backward they share one group's tiles)
+    int blocks;           // backward: workgroups over the channels of one group of b and c
+    int chunks;           // of a row
+    int segments, seg;    // parts of a row worked on at once, chunks of each
+};
+
+// The recurrence runs through a row.  Rows and channels alone are too few waves where a batch is small, so a row
+// is cut into segments: each is first run from a zero state (half of the work again), then from the state that the
+// segments before it leave.
+inline SsmPlan ssm_plan(int64_t batch, int64_t length, int d, int n, int groups, bool backward) {
+    SsmPlan p{};
+    p.ng = ssm_state_groups(n);
+    p.waves = p.ng == 1 && backward ? 2 : 4;
+    p.tiles = (int)ceil_div(d / groups, 128 / p.ng);
+    p.blocks = (int)ceil_div(p.tiles, p.waves);
+    p.chunks = (int)ceil_div(length, SSM_TOK);
+    const int64_t want = backward ? 2048 : 4096;
+    const int64_t units = std::max<int64_t>(1, batch * groups * (backward ? (int64_t)p.blocks * p.waves : p.tiles));
+    const int64_t s = std::min<int64_t>({ceil_div(want, units), 64, std::max(1, p.chunks)});
+    p.seg = (int)ceil_div(std::max(1, p.chunks), s);
+    p.segments = (int)ceil_div(std::max(1, p.chunks), p.seg);
+    return p;
+}
+
+inline bool ssm_shape(int64_t batch, int64_t length, int d, int n, int groups) {
+    return batch >= 0 && length >= 0 && length <= 0x7fffff00 && batch <= 0x7fffffff && (length == 0 || batch <= 0x7fffffff / length) &&
+           d >= 1 && groups >= 1 && d % groups == 0 && n >= 1 && n <= SSM_MOST_N;
+}
+
+// Sizes that the launches cover: workgroups of 256 threads, and element counts within 62 bits.
+inline bool ssm_fits(int64_t batch, int64_t length, int d, int n, int groups) {
+    if (!ssm_shape(batch, length, d, n, groups)) return false;
+    const int64_t chunks = ceil_div(std::max<int64_t>(length, 1), SSM_TOK), most = MOST_THREADS / 256;
+    const SsmPlan f = ssm_plan(batch, length, d, n, groups, false), b = ssm_plan(batch, length, d, n, groups, true);
+    const __int128 state = (__int128)batch * chunks * d * SSM_MOST_N * 4, rows = (__int128)batch * length * groups;
+    return (__int128)batch * groups * f.tiles * f.segments <= most && (__int128)batch * groups * b.blocks * b.segments <= most &&
+           (__int128)batch * d * 16 <= MOST_THREADS && rows * SSM_MOST_N * 2 <= MOST_THREADS && (__int128)d * SSM_MOST_N * 64 <= MOST_THREADS &&
+           state < ((__int128)1 << 62) && rows * b.blocks * SSM_MOST_N * 8 < ((__int128)1 << 62);
+}
+
+}  // namespace lrs

@@ -2,7 +2,7 @@
 of the C ABI in include/lm_ops.h.
 
 Block norms with their gate and residual scale, the softmax cross entropy of a
-linear head, and the AdamW step over many tensors.  Argument checks and
+linear head, the AdamW step over many tensors, and the embedding lookup.  Argument checks and
 marshalling only: every step runs in the HIP kernels of libsamu_scan.so, on
 the current stream or the one given.  The differentiable forms are in
 autograd.py.
@@ -63,6 +63,12 @@ def lib():
     L.lm_linear_ce_bwd.restype = i
     L.lm_adamw_step.argtypes = [i, i, i, i] + [vp] * 9 + [dbl] * 4 + [i64, vp]
     L.lm_adamw_step.restype = i
+    L.lm_embed_fwd.argtypes = [i64, i, i64, i, i, dbl, vp, vp, vp, vp]
+    L.lm_embed_fwd.restype = i
+    L.lm_embed_bwd_workspace_bytes.argtypes = [i64, i, i64]
+    L.lm_embed_bwd_workspace_bytes.restype = sz
+    L.lm_embed_bwd.argtypes = [i64, i, i64, i, i, dbl, vp, vp, i64, i, vp, vp, sz, vp]
+    L.lm_embed_bwd.restype = i
     _lib = L
     return L
 
@@ -415,3 +421,74 @@ def adamw_state(p, bits=32):
     s = dict(dtype=_F32, device=p.device)
     return dict(m=torch.zeros(p.shape, **z).view(_F8), v=torch.zeros(p.shape, **z).view(_F8),
                 m_scale=torch.zeros(blocks, **s), v_scale=torch.zeros(blocks, **s))
+
+
+# -------------------------------------------------------- embedding lookup ---
+def embed_fwd(tokens, w, *, scale=1.0, out_dtype=None, out=None, stream=None):
+    """Rows of an embedding: out_t = scale * w[tokens_t].
+
+    tokens [...] int64, w [v, d] BF16 or FP32.  A negative token is padding: its
+    row of out is zero (a token >= v: NaN).  out_dtype: BF16 or FP32, w's if
+    None.  Returns out [..., d]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return embed_fwd(tokens, w, scale=scale, out_dtype=out_dtype, out=out)
+    _want(tokens, "tokens", torch.int64)
+    _want(w, "w", _DTYPES)
+    if w.dim() != 2 or w.shape[0] < 1 or w.shape[1] < 1:
+        raise ValueError(f"w must be [v, d] with v, d >= 1, got shape {tuple(w.shape)}")
+    _dense(tokens, "tokens")
+    _dense(w, "w")
+    v, d = w.shape
+    given = out
+    if out_dtype is None:
+        out_dtype = w.dtype if out is None else out.dtype
+    _code(out_dtype)
+    if out is None:
+        out = torch.empty((*tokens.shape, d), dtype=out_dtype, device=w.device)
+    _want(out, "out", out_dtype, (*tokens.shape, d))
+    _dense(out, "out")
+    _same_device(w, tokens=tokens, out=out)
+    st = lib().lm_embed_fwd(tokens.numel(), d, v, _code(w.dtype), _code(out_dtype), scale, _p(tokens), _p(w), _p(out), _stream(None))
+    _check(st, "lm_embed_fwd")
+    _written(given)
+    return out
+
+
+def embed_bwd(tokens, dout, v, *, scale=1.0, grad_dtype=_BF16, dw=None, accumulate=False, workspace=None, stream=None):
+    """Gradient of embed_fwd's w [v, d] for the cotangent dout [..., d] (BF16 or
+    FP32; rows may lie apart): dw_j = scale * the sum of dout over the tokens j,
+    FP32 sums in an order that the tokens alone decide, rounded once.  dw is of
+    grad_dtype, zero where no token is.  accumulate: the sums are added to the dw given, before the
+    rounding; rows without tokens stay as they are.  Returns dw."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return embed_bwd(tokens, dout, v, scale=scale, grad_dtype=grad_dtype, dw=dw, accumulate=accumulate, workspace=workspace)
+    _want(tokens, "tokens", torch.int64)
+    _want(dout, "dout", _DTYPES)
+    if dout.dim() < 1 or dout.shape[:-1] != tokens.shape or dout.shape[-1] < 1:
+        raise ValueError(f"dout must be [..., d] with the tokens' shape in front, got shapes {tuple(dout.shape)} and {tuple(tokens.shape)}")
+    _dense(tokens, "tokens")
+    n, d, v = tokens.numel(), dout.shape[-1], int(v)
+    if accumulate and dw is None:
+        raise ValueError("accumulate needs a dw to add to")
+    given = dw
+    if dw is None:
+        if v < 1:
+            raise ValueError(f"v must be at least 1, got {v}")
+        _code(grad_dtype)
+        dw = torch.empty((v, d), dtype=grad_dtype, device=dout.device)
+    _want(dw, "dw", _DTYPES, (v, d))
+    _dense(dw, "dw")
+    _same_device(dout, tokens=tokens, dw=dw)
+    need = lib().lm_embed_bwd_workspace_bytes(n, d, v)
+    if need == 0:
+        raise ValueError(f"unsupported shape: {n} tokens, width {d}, vocabulary {v}")
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dout.device)
+    _want_bytes(workspace, "workspace", need)
+    st = lib().lm_embed_bwd(n, d, v, _code(dout.dtype), _code(dw.dtype), scale, _p(tokens), _p(dout), _row_stride(dout, "dout"), int(bool(accumulate)),
+                            _p(dw), _p(workspace), _nbytes(workspace), _stream(None))
+    _check(st, "lm_embed_bwd")
+    _written(given)
+    return dw
