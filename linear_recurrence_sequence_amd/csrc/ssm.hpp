@@ -86,27 +86,21 @@ __device__ __forceinline__ float softplus_of(float x, float* slope) {
 typedef f32x2_t __attribute__((aligned(4))) f32x2_a4;
 typedef uint32_t __attribute__((aligned(2))) u32_a2;
 
-// Two channels of a row as they lie in memory; where a group's channels are odd in number (pair false) the second may be another
-// than the next one.
+// Two channels of a row as they lie in memory.
 template <class T>
 struct Pair;
 template <>
 struct Pair<uint16_t> {
     uint32_t w;
-    static __device__ __forceinline__ Pair load(const uint16_t* row, int i, int k, bool pair) {
-        if (pair) return {*reinterpret_cast<const u32_a2*>(row + i)};
-        return {(uint32_t)row[i] | (uint32_t)row[k] << 16};
-    }
-    __device__ __forceinline__ float2 get() const { return make_float2(bf16_lo(w), bf16_hi(w)); }
+    static __device__ __forceinline__ Pair load(const uint16_t* base, uint32_t off) { return {*reinterpret_cast<const u32_a2*>(base + off)}; }
+    // odd: both are the second one
+    __device__ __forceinline__ float2 get(bool odd) const { return make_float2(odd ? bf16_hi(w) : bf16_lo(w), bf16_hi(w)); }
 };
 template <>
 struct Pair<float> {
     f32x2_t w;
-    static __device__ __forceinline__ Pair load(const float* row, int i, int k, bool pair) {
-        if (pair) return {*reinterpret_cast<const f32x2_a4*>(row + i)};
-        return {f32x2_t{row[i], row[k]}};
-    }
-    __device__ __forceinline__ float2 get() const { return make_float2(w[0], w[1]); }
+    static __device__ __forceinline__ Pair load(const float* base, uint32_t off) { return {*reinterpret_cast<const f32x2_a4*>(base + off)}; }
+    __device__ __forceinline__ float2 get(bool odd) const { return make_float2(odd ? w[1] : w[0], w[1]); }
 };
 
 __device__ __forceinline__ float value_of(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
@@ -114,26 +108,25 @@ __device__ __forceinline__ float value_of(float v) { return v; }
 __device__ __forceinline__ void store_value(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_value(uint16_t* p, float v) { *p = (uint16_t)pack_bf16x2(v, v); }
 
-// Stores the pair (ok0, ok1: which of it exist).
-__device__ __forceinline__ void store_pair(uint16_t* p, float2 v, bool ok0, bool ok1, bool pair) {
+// Stores a pair, or the first of it where it has no partner.
+__device__ __forceinline__ void store_pair(uint16_t* p, float2 v, bool ok0, bool ok1) {
     const uint32_t w = pack_bf16x2(v.x, v.y);
-    if (pair) {
-        if (ok0) __builtin_nontemporal_store(w, reinterpret_cast<u32_a2*>(p));
-    } else {
-        if (ok0) p[0] = (uint16_t)w;
-        if (ok1) p[1] = (uint16_t)(w >> 16);
-    }
+    if (ok1) __builtin_nontemporal_store(w, reinterpret_cast<u32_a2*>(p));
+    else if (ok0) *p = (uint16_t)w;
 }
-__device__ __forceinline__ void store_pair(float* p, float2 v, bool ok0, bool ok1, bool pair) {
-    if (pair) {
-        if (ok0) __builtin_nontemporal_store(f32x2_t{v.x, v.y}, reinterpret_cast<f32x2_a4*>(p));
-    } else {
-        if (ok0) p[0] = v.x;
-        if (ok1) p[1] = v.y;
-    }
+__device__ __forceinline__ void store_pair(float* p, float2 v, bool ok0, bool ok1) {
+    if (ok1) __builtin_nontemporal_store(f32x2_t{v.x, v.y}, reinterpret_cast<f32x2_a4*>(p));
+    else if (ok0) *p = v.x;
 }
 
 // ------------------------------------------------- sums over lane groups ---
+// The value of the lane whose number differs in bit M (of a row of 16 lanes; M = 4: of lanes that hold what their quad's others do).
+template <int M>
+__device__ __forceinline__ float row_xor(float v) {
+    constexpr int ctrl = M == 1 ? 0xb1 : M == 2 ? 0x4e : M == 4 ? 0x141 : 0x128;  // quad [1,0,3,2], [2,3,0,1]; mirror of 8; rotation by 8
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), ctrl, 0xf, 0xf, true));
+}
+
 // Two values to one: lanes with bit M of their number clear get the sum of a over their pair of lanes, the others that of b.
 template <int M>
 __device__ __forceinline__ float pair_sum(float a, float b) {
@@ -145,6 +138,7 @@ __device__ __forceinline__ float pair_sum(float a, float b) {
         return __uint_as_float(r[0]) + __uint_as_float(r[1]);
     } else {
         const bool up = threadIdx.x & M;
+        if constexpr (M == 8) return (up ? b : a) + row_xor<8>(up ? a : b);
         return (up ? b : a) + __shfl_xor(up ? a : b, M);
     }
 }

@@ -24,178 +24,142 @@ struct Chunk {
     Pair<T> u[Q], dt[Q], z[Q];
     T b[NG], c[NG];
 };
-template <class T, int NG, bool SUM>
-__device__ __forceinline__ void load_chunk(const SsmArgs& a, const Place& p, int t0, Chunk<T, NG>& v) {
-    const int lane = threadIdx.x & 63, g = lane / Lay<NG>::J;
-    const int64_t row0 = (int64_t)p.b * a.length;
+template <class T, int NG, bool GATE, bool SUM>
+__device__ __forceinline__ void load_chunk(const SsmArgs& a, const Place& p, int chunk, Chunk<T, NG>& v) {
+    const int64_t row0 = (int64_t)p.b * a.length + chunk * SSM_TOK;
+    const int left = a.length - chunk * SSM_TOK, g = fresh_lane() / Lay<NG>::J;
+    const T *u = rows_at<T>(a.u, row0, a.u_stride), *dt = rows_at<T>(a.dt, row0, a.dt_stride), *z = rows_at<T>(a.z, row0, a.z_stride);
 #pragma unroll
     for (int q = 0; q < Lay<NG>::Q; ++q) {
-        const int64_t row = row0 + min(t0 + q * NG + g, a.length - 1);
-        v.u[q] = Pair<T>::load(static_cast<const T*>(a.u) + row * a.u_stride, p.i, p.k, p.pair);
-        v.dt[q] = Pair<T>::load(static_cast<const T*>(a.dt) + row * a.dt_stride, p.i, p.k, p.pair);
-        if (!SUM && a.z) v.z[q] = Pair<T>::load(static_cast<const T*>(a.z) + row * a.z_stride, p.i, p.k, p.pair);
+        const int r = min(q * NG + g, left - 1);
+        v.u[q] = Pair<T>::load(u, row_off(r, a.u_stride, p.i));
+        v.dt[q] = Pair<T>::load(dt, row_off(r, a.dt_stride, p.i));
+        if (!SUM && GATE) v.z[q] = Pair<T>::load(z, row_off(r, a.z_stride, p.i));
     }
-#pragma unroll
-    for (int e = 0; e < NG; ++e) {
-        const int x = e * 64 + lane, t = x / Lay<NG>::N4, n = min(x % Lay<NG>::N4, a.n - 1);
-        const int64_t row = row0 + min(t0 + t, a.length - 1);
-        v.b[e] = static_cast<const T*>(a.b)[row * a.b_stride + p.gr * a.n + n];
-        if (!SUM) v.c[e] = static_cast<const T*>(a.c)[row * a.c_stride + p.gr * a.n + n];
-    }
+    load_group<T, NG>(a.b, a.b_stride, row0, left, p.gr, a.n, v.b);
+    if (!SUM) load_group<T, NG>(a.c, a.c_stride, row0, left, p.gr, a.n, v.c);
 }
 
 // SUM: a segment from a zero state, for the product of its decays and the state that leaves it.
-template <class T, int NG, bool SUM>
+template <class T, int NG, bool GATE, bool SUM>
 __global__ __launch_bounds__(256) void ssm_fwd_kernel(const SsmArgs a) {
     using Y = Lay<NG>;
     constexpr int Q = Y::Q, J = Y::J;
-    __shared__ float4 s_dt[4][SSM_TOK * J];            // s, s u of two channels
-    __shared__ float4 s_b[4][SSM_TOK * NG], s_c[4][SUM ? 1 : SSM_TOK * NG];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane / J, j = lane % J;
+    struct Wave {
+        float4 su[SSM_TOK * J];                        // s, s u of two channels
+        float4 b[SSM_TOK * NG], c[SUM ? 1 : SSM_TOK * NG];
+    };
+    __shared__ Wave waves[4];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tiles = a.plan.tiles * a.groups, segs = SUM ? a.plan.segments - 1 : a.plan.segments;
     const int64_t unit = (int64_t)blockIdx.x * 4 + wave;
     if (unit >= (int64_t)tiles * segs * a.batch) return;  // waves do not wait for each other
     const int tile = (int)(unit % tiles), seg = (int)(unit / tiles % segs), b = (int)(unit / tiles / segs);
     const Place p = place_of<NG>(a, tile % a.plan.tiles, tile / a.plan.tiles, seg, b);
     const int len = length_of(a, b);
+    Wave& m = waves[wave];
 
     float A[2][4], h[2][4];
     bool okn[4];
+    load_rates(a, p, A, okn);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        const int n = 4 * g + s;
-        okn[s] = n < a.n;
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            A[c][s] = (c ? p.ok1 : p.ok0) && okn[s] ? LOG2E * a.a[(int64_t)(p.c0 + c) * a.n + n] : 0.0f;
+        for (int s = 0; s < 4; ++s) {
             h[c][s] = 0.0f;
+            if (SUM || !(c ? p.ok1 : p.ok0) || !okn[s]) continue;
+            const int n = 4 * p.g + s;
+            if (a.h0) h[c][s] = a.h0[((int64_t)b * a.d + p.c0 + c) * a.n + n];
+            h[c][s] = through_segments(a, p, c, n, 0, seg, 1, h[c][s]);  // what those before this one leave
         }
-    }
-    if (!SUM) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                if (!(c ? p.ok1 : p.ok0) || !okn[s]) continue;
-                const int n = 4 * g + s;
-                if (a.h0) h[c][s] = a.h0[((int64_t)b * a.d + p.c0 + c) * a.n + n];
-                // the state that the segments before this one leave
-                const float* at = a.part + (int64_t)b * a.plan.segments * 2 * a.n * a.d + (int64_t)n * a.d + p.c0 + c;
-                for (int i = 0; i < seg; ++i, at += (int64_t)2 * a.n * a.d) {
-                    const float decay = at[0], left = at[(int64_t)a.n * a.d];
-                    h[c][s] = decay == 0.0f ? left : fmaf(decay, h[c][s], left);  // 0: also what starts anew, whatever was before
-                }
-            }
-    }
-    const float2 bias = a.dt_bias ? make_float2(a.dt_bias[p.i], a.dt_bias[p.k]) : make_float2(0.f, 0.f);
-    const float2 skip = !SUM && a.skip ? make_float2(a.skip[p.i], a.skip[p.k]) : make_float2(0.f, 0.f);
+    const float2 bias = load_two(a.dt_bias, p), skip = load_two(SUM ? nullptr : a.skip, p);
     float2 total = make_float2(0.f, 0.f);
     bool anew = false;
     const int first = seg * a.plan.seg, last = min(first + a.plan.seg, a.plan.chunks);
     Chunk<T, NG> v;
-    if (first < last) load_chunk<T, NG, SUM>(a, p, first * SSM_TOK, v);
+    if (first < last) load_chunk<T, NG, GATE, SUM>(a, p, first, v);
     for (int chunk = first; chunk < last; ++chunk) {
-        const int t0 = chunk * SSM_TOK;
+        const int lane = fresh_lane(), g = lane / J, j = lane % J;
+        const int t0 = chunk * SSM_TOK, live = len - t0, left = a.length - t0;
         if (!SUM && a.saved) {
-            float* at = a.saved + (((int64_t)b * a.plan.chunks + chunk) * a.n + 4 * g) * a.d + p.c0;
+            float* at = a.saved + ((int64_t)b * a.plan.chunks + chunk) * a.n * a.d;
 #pragma unroll
-            for (int s = 0; s < 4; ++s, at += a.d)
-                if (okn[s]) store_pair(at, make_float2(h[0][s], h[1][s]), p.ok0, p.ok1, p.pair);
+            for (int s = 0; s < 4; ++s)
+                if (okn[s]) store_pair(at + ((uint32_t)((4 * g + s) * a.d) + (uint32_t)p.c0), make_float2(h[0][s], h[1][s]), p.ok0, p.ok1);
         }
         const uint32_t resets = resets_of(a, b, t0, len);
         anew |= resets != 0;
         float2 us[Q], gate[Q];
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            const int t = t0 + q * NG + g;
-            const float2 u = v.u[q].get(), x = v.dt[q].get();
+            const float2 u = v.u[q].get(p.odd), x = v.dt[q].get(p.odd);
             float slope, s0 = x.x + bias.x, s1 = x.y + bias.y;
             if (a.softplus) s0 = softplus_of(s0, &slope), s1 = softplus_of(s1, &slope);
-            const bool on0 = t < len && p.ok0, on1 = t < len && p.ok1;
+            const bool on = q * NG + g < live, on0 = on && p.ok0, on1 = on && p.ok1;
             const float4 w = make_float4(on0 ? s0 : 0.0f, on0 ? s0 * u.x : 0.0f, on1 ? s1 : 0.0f, on1 ? s1 * u.y : 0.0f);
-            s_dt[wave][(q * NG + g) * J + j] = w;
+            m.su[q * 64 + lane] = w;
             if (SUM) {
                 total.x += w.x, total.y += w.z;
             } else {
                 us[q] = u;
                 gate[q] = make_float2(1.0f, 1.0f);
-                if (a.z) {
-                    const float2 z = v.z[q].get();
+                if (GATE) {
+                    const float2 z = v.z[q].get(p.odd);
                     gate[q] = make_float2(z.x * sigmoid_of(z.x), z.y * sigmoid_of(z.y));
                 }
             }
         }
-#pragma unroll
-        for (int e = 0; e < NG; ++e) {
-            const int x = e * 64 + lane;
-            const bool on = t0 + x / Y::N4 < len && x % Y::N4 < a.n;
-            reinterpret_cast<float*>(s_b[wave])[x] = on ? value_of(v.b[e]) : 0.0f;
-            if (!SUM) reinterpret_cast<float*>(s_c[wave])[x] = on ? value_of(v.c[e]) : 0.0f;
-        }
-        if (chunk + 1 < last) load_chunk<T, NG, SUM>(a, p, t0 + SSM_TOK, v);
+        put_group<T, NG>(v.b, m.b, live, a.n);
+        if (!SUM) put_group<T, NG>(v.c, m.c, live, a.n);
+        if (chunk + 1 < last) load_chunk<T, NG, GATE, SUM>(a, p, chunk + 1, v);
         wave_lds_sync();
         // a chunk without a sequence's start, as most are, runs free of branches
         const auto walk = [&](auto starts) {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            float y0[NG], y1[NG];
+            for (int q = 0; q < Q; ++q) {
+                float y0[NG], y1[NG];
 #pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                const int t = q * NG + i;
-                const float4 x = s_dt[wave][t * J + j], B = s_b[wave][t * NG + g];
-                if (decltype(starts)::value && (resets >> t & 1u)) {
+                for (int i = 0; i < NG; ++i) {
+                    const int t = q * NG + i;
+                    const float4 x = m.su[t * J + j], B = m.b[t * NG + g];
+                    if (decltype(starts)::value && (resets >> t & 1u)) {
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) h[0][s] = h[1][s] = 0.0f;
-                }
-                const float bs[4] = {B.x, B.y, B.z, B.w};
+                        for (int s = 0; s < 4; ++s) h[0][s] = h[1][s] = 0.0f;
+                    }
+                    const float bs[4] = {B.x, B.y, B.z, B.w};
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    h[0][s] = fmaf(__builtin_amdgcn_exp2f(x.x * A[0][s]), h[0][s], x.y * bs[s]);
-                    h[1][s] = fmaf(__builtin_amdgcn_exp2f(x.z * A[1][s]), h[1][s], x.w * bs[s]);
+                    for (int s = 0; s < 4; ++s) {
+                        h[0][s] = fmaf(__builtin_amdgcn_exp2f(x.x * A[0][s]), h[0][s], x.y * bs[s]);
+                        h[1][s] = fmaf(__builtin_amdgcn_exp2f(x.z * A[1][s]), h[1][s], x.w * bs[s]);
+                    }
+                    if (!SUM) {
+                        const float4 C = m.c[t * NG + g];
+                        y0[i] = fmaf(C.w, h[0][3], fmaf(C.z, h[0][2], fmaf(C.y, h[0][1], C.x * h[0][0])));
+                        y1[i] = fmaf(C.w, h[1][3], fmaf(C.z, h[1][2], fmaf(C.y, h[1][1], C.x * h[1][0])));
+                    }
+                    if (t % 2) __builtin_amdgcn_sched_barrier(0);  // keeps the reads of later tokens from taking all registers
                 }
                 if (!SUM) {
-                    const float4 C = s_c[wave][t * NG + g];
-                    y0[i] = fmaf(C.w, h[0][3], fmaf(C.z, h[0][2], fmaf(C.y, h[0][1], C.x * h[0][0])));
-                    y1[i] = fmaf(C.w, h[1][3], fmaf(C.z, h[1][2], fmaf(C.y, h[1][1], C.x * h[1][0])));
+                    const int r = q * NG + g;
+                    const float r0 = group_sum<NG>(y0), r1 = group_sum<NG>(y1);
+                    const bool on = r < live;  // padding: whatever u and z hold
+                    const float2 y = make_float2(on ? fmaf(skip.x, us[q].x, r0) * gate[q].x : 0.0f, on ? fmaf(skip.y, us[q].y, r1) * gate[q].y : 0.0f);
+                    store_pair(rows_at<T>(a.y, (int64_t)b * a.length + t0, a.d) + row_off(r, a.d, p.c0), y, r < left && p.ok0, r < left && p.ok1);
                 }
             }
-            if (!SUM) {
-                const int t = t0 + q * NG + g;
-                const float r0 = group_sum<NG>(y0), r1 = group_sum<NG>(y1);
-                const bool on = t < len;  // padding: whatever u and z hold
-                const float2 y = make_float2(on ? fmaf(skip.x, us[q].x, r0) * gate[q].x : 0.0f,
-                                             on ? fmaf(skip.y, us[q].y, r1) * gate[q].y : 0.0f);
-                if (t < a.length)
-                    store_pair(static_cast<T*>(a.y) + ((int64_t)b * a.length + t) * a.d + p.c0, y, p.ok0, p.ok1, p.pair);
-            }
-        }
         };
         if (resets) walk(std::true_type{});
         else walk(std::false_type{});
         wave_lds_sync();
     }
     if (SUM) {
-        // the tokens' lanes hold parts of the sum of s
-#pragma unroll
-        for (int o = 32; o >= J; o >>= 1) {
-            total.x += __shfl_xor(total.x, o);
-            total.y += __shfl_xor(total.y, o);
-        }
-        float* at = a.part + (((int64_t)b * a.plan.segments + seg) * 2 * a.n + 4 * g) * a.d + p.c0;
-#pragma unroll
-        for (int s = 0; s < 4; ++s, at += a.d) {
-            if (!okn[s]) continue;
-            const float d0 = anew ? 0.0f : __builtin_amdgcn_exp2f(total.x * A[0][s]);
-            const float d1 = anew ? 0.0f : __builtin_amdgcn_exp2f(total.y * A[1][s]);
-            store_pair(at, make_float2(d0, d1), p.ok0, p.ok1, p.pair);
-            store_pair(at + (int64_t)a.n * a.d, make_float2(h[0][s], h[1][s]), p.ok0, p.ok1, p.pair);
-        }
+        put_segment<NG>(a, p, A, okn, total, anew, h);
     } else if (seg == segs - 1) {
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-                if ((c ? p.ok1 : p.ok0) && okn[s]) a.h[((int64_t)b * a.d + p.c0 + c) * a.n + 4 * g + s] = h[c][s];
+                if ((c ? p.ok1 : p.ok0) && okn[s]) a.h[((int64_t)b * a.d + p.c0 + c) * a.n + 4 * p.g + s] = h[c][s];
     }
 }
 
@@ -254,9 +218,11 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(const SsmArgs a) {
 template <class T, int NG>
 void launch_fwd(const SsmArgs& a, hipStream_t s) {
     const int64_t tiles = (int64_t)a.plan.tiles * a.groups * a.batch;
+    const dim3 g((unsigned)ceil_div(tiles * a.plan.segments, 4)), b(256);
     if (a.plan.segments > 1)
-        LRS_LAUNCH(K_SSM_SUMMARY, (ssm_fwd_kernel<T, NG, true>), dim3((unsigned)ceil_div(tiles * (a.plan.segments - 1), 4)), dim3(256), 0, s, a);
-    LRS_LAUNCH(K_SSM_SCAN, (ssm_fwd_kernel<T, NG, false>), dim3((unsigned)ceil_div(tiles * a.plan.segments, 4)), dim3(256), 0, s, a);
+        LRS_LAUNCH(K_SSM_SUMMARY, (ssm_fwd_kernel<T, NG, false, true>), dim3((unsigned)ceil_div(tiles * (a.plan.segments - 1), 4)), b, 0, s, a);
+    if (a.z) LRS_LAUNCH(K_SSM_SCAN, (ssm_fwd_kernel<T, NG, true, false>), g, b, 0, s, a);
+    else LRS_LAUNCH(K_SSM_SCAN, (ssm_fwd_kernel<T, NG, false, false>), g, b, 0, s, a);
 }
 template <class T>
 void launch_fwd_any(const SsmArgs& a, hipStream_t s) {

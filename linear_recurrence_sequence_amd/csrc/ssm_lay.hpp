@@ -11,23 +11,31 @@ struct Lay {
     static constexpr int J = 64 / NG, CH = 2 * J, N4 = SSM_STATES * NG, Q = SSM_TOK / NG;
 };
 
-// A wave's row and segment, its lane's channels.
+// The lane's number, formed anew: what is derived from it inside a loop stays there, where keeping a register for each of many addresses
+// would cost more than a few integer operations a chunk.
+__device__ __forceinline__ int fresh_lane() {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
+// A wave's row and segment, its lane's part of the channels and states.
 struct Place {
-    int b, seg, gr, c0, end;     // row, segment, group of b and c, the lane's first channel, the group's end
-    int i, k;                    // channels that the lane loads: its own, or existing ones in their place
-    bool ok0, ok1, pair;
+    int b, seg, gr, c0;          // row, segment, group of b and c, the lane's first channel
+    int i;                       // first of the two channels that the lane loads: its own, or existing ones
+    bool ok0, ok1, odd;          // which of its channels exist; odd: the first is the second one loaded (a group's last, without a partner)
+    int g, j;                    // the lane's group of states and pair of channels
 };
 template <int NG>
 __device__ __forceinline__ Place place_of(const SsmArgs& a, int tile, int gr, int seg, int b) {
-    const int j = (threadIdx.x & 63) % Lay<NG>::J;
+    const int lane = threadIdx.x & 63, end = (gr + 1) * a.per;
     Place p;
     p.b = b, p.seg = seg, p.gr = gr;
-    p.end = (gr + 1) * a.per;
-    p.c0 = gr * a.per + tile * Lay<NG>::CH + 2 * j;
-    p.ok0 = p.c0 < p.end, p.ok1 = p.c0 + 1 < p.end;
-    p.pair = a.per % 2 == 0;
-    p.i = min(p.c0, p.end - (p.pair ? 2 : 1));
-    p.k = min(p.c0 + 1, p.end - 1);
+    p.g = lane / Lay<NG>::J, p.j = lane % Lay<NG>::J;
+    p.c0 = gr * a.per + tile * Lay<NG>::CH + 2 * p.j;
+    p.ok0 = p.c0 < end, p.ok1 = p.c0 + 1 < end;
+    p.i = max(min(p.c0, end - 2), 0);  // d is at least 2
+    p.odd = p.c0 == p.i + 1;
     return p;
 }
 
@@ -41,6 +49,89 @@ __device__ __forceinline__ uint32_t resets_of(const SsmArgs& a, int b, int t0, i
     const int t = t0 + (threadIdx.x & 63);
     const bool r = t < min(t0 + SSM_TOK, len) && a.reset[(int64_t)b * a.length + t] != 0;
     return (uint32_t)__ballot(r);
+}
+
+// A chunk's rows of one tensor: a uniform base and a lane's offset of 32 bits, of a row number below 16 and a
+// distance below 2^22 elements (SSM_MOST_STRIDE).
+template <class T>
+__device__ __forceinline__ const T* rows_at(const void* p, int64_t row, int64_t stride) {
+    return static_cast<const T*>(p) + row * stride;
+}
+template <class T>
+__device__ __forceinline__ T* rows_at(void* p, int64_t row, int64_t stride) {
+    return static_cast<T*>(p) + row * stride;
+}
+__device__ __forceinline__ uint32_t row_off(int r, int64_t stride, int col) { return __umul24((uint32_t)r, (uint32_t)stride) + (uint32_t)col; }
+
+// What b or c hold for a chunk, a lane's part: element e * 64 + lane of [SSM_TOK][N4].
+template <class T, int NG>
+__device__ __forceinline__ void load_group(const void* p, int64_t stride, int64_t row0, int left, int gr, int n, T (&v)[NG]) {
+    const T* at = rows_at<T>(p, row0, stride) + gr * n;
+    const int lane = fresh_lane();
+#pragma unroll
+    for (int e = 0; e < NG; ++e) {
+        const int x = e * 64 + lane;
+        v[e] = at[row_off(min(x / Lay<NG>::N4, left - 1), stride, min(x % Lay<NG>::N4, n - 1))];
+    }
+}
+// To LDS in FP32, zero for padding (from token `live` of the chunk on) and for states that do not exist.
+template <class T, int NG>
+__device__ __forceinline__ void put_group(const T (&v)[NG], float4* to, int live, int n) {
+    const int lane = fresh_lane();
+#pragma unroll
+    for (int e = 0; e < NG; ++e) {
+        const int x = e * 64 + lane;
+        reinterpret_cast<float*>(to)[x] = x / Lay<NG>::N4 < live && x % Lay<NG>::N4 < n ? value_of(v[e]) : 0.0f;
+    }
+}
+
+// The decays' factors of a lane's states, times log2 e.
+__device__ __forceinline__ void load_rates(const SsmArgs& a, const Place& p, float (&A)[2][4], bool (&okn)[4]) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const int n = 4 * p.g + s;
+        okn[s] = n < a.n;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            A[c][s] = (c ? p.ok1 : p.ok0) && okn[s] ? LOG2E * a.a[(int64_t)(p.c0 + c) * a.n + n] : 0.0f;
+    }
+}
+// Two of a vector's values.
+__device__ __forceinline__ float2 load_two(const float* v, const Place& p) {
+    if (!v) return make_float2(0.f, 0.f);
+    return make_float2(v[p.odd ? p.i + 1 : p.i], v[p.i + 1]);
+}
+
+// What a segment from nothing leaves: the product of its decays (0 behind a sequence's start) and its state or cotangent.
+template <int NG>
+__device__ __forceinline__ void put_segment(const SsmArgs& a, const Place& p, const float (&A)[2][4], const bool (&okn)[4], float2 total,
+                                            bool anew, const float (&h)[2][4]) {
+    // the tokens' lanes hold parts of the sum of s
+#pragma unroll
+    for (int o = 32; o >= Lay<NG>::J; o >>= 1) {
+        total.x += __shfl_xor(total.x, o);
+        total.y += __shfl_xor(total.y, o);
+    }
+    float* at = a.part + (((int64_t)p.b * a.plan.segments + p.seg) * 2 * a.n + 4 * p.g) * a.d + p.c0;
+#pragma unroll
+    for (int s = 0; s < 4; ++s, at += a.d) {
+        if (!okn[s]) continue;
+        const float d0 = anew ? 0.0f : __builtin_amdgcn_exp2f(total.x * A[0][s]);
+        const float d1 = anew ? 0.0f : __builtin_amdgcn_exp2f(total.y * A[1][s]);
+        store_pair(at, make_float2(d0, d1), p.ok0, p.ok1);
+        store_pair(at + (int64_t)a.n * a.d, make_float2(h[0][s], h[1][s]), p.ok0, p.ok1);
+    }
+}
+// h (a state's part for one channel) through the segments from, from + step, .. up to `to` (not included).  A product of 0 also stands for a
+// sequence's start, behind which nothing counts, whatever it was.
+__device__ __forceinline__ float through_segments(const SsmArgs& a, const Place& p, int c, int n, int from, int to, int step, float h) {
+    const int64_t one = (int64_t)2 * a.n * a.d, half = (int64_t)a.n * a.d;
+    const float* at = a.part + ((int64_t)p.b * a.plan.segments + from) * one + (int64_t)n * a.d + p.c0 + c;
+    for (int i = from; i != to; i += step, at += step * one) {
+        const float decay = at[0], left = at[half];
+        h = decay == 0.0f ? left : fmaf(decay, h, left);
+    }
+    return h;
 }
 
 }  // namespace lrs

@@ -13,6 +13,7 @@ namespace lrs {
 constexpr int SSM_TOK = 16;       // tokens of a chunk: a state is kept before each
 constexpr int SSM_STATES = 4;     // states of a lane, for two channels
 constexpr int SSM_MOST_N = 64;
+constexpr int64_t SSM_MOST_STRIDE = (1 << 22) - 1;  // a chunk's rows are addressed by 24-bit products and 32-bit offsets
 
 // A wave takes 128 / ng channels and all states: its lanes are ng groups (of
 // SSM_STATES states each) of 64 / ng channel pairs.
@@ -51,7 +52,7 @@ inline SsmPlan ssm_plan(int64_t batch, int64_t length, int d, int n, int groups,
 
 inline bool ssm_shape(int64_t batch, int64_t length, int d, int n, int groups) {
     return batch >= 0 && length >= 0 && length <= 0x7fffff00 && batch <= 0x7fffffff && (length == 0 || batch <= 0x7fffffff / length) &&
-           d >= 1 && groups >= 1 && d % groups == 0 && n >= 1 && n <= SSM_MOST_N;
+           d >= 2 && d <= (1 << 21) && groups >= 1 && d % groups == 0 && n >= 1 && n <= SSM_MOST_N;
 }
 
 // Sizes that the launches cover: workgroups of 256 threads, and element counts within 62 bits.
