@@ -86,21 +86,20 @@ __device__ __forceinline__ float softplus_of(float x, float* slope) {
 typedef f32x2_t __attribute__((aligned(4))) f32x2_a4;
 typedef uint32_t __attribute__((aligned(2))) u32_a2;
 
-// Two channels of a row as they lie in memory.
+// Two channels of a row as they lie in memory, at a uniform base and a lane's offset in bytes.
 template <class T>
 struct Pair;
 template <>
 struct Pair<uint16_t> {
     uint32_t w;
-    static __device__ __forceinline__ Pair load(const uint16_t* base, uint32_t off) { return {*reinterpret_cast<const u32_a2*>(base + off)}; }
-    // odd: both are the second one
-    __device__ __forceinline__ float2 get(bool odd) const { return make_float2(odd ? bf16_hi(w) : bf16_lo(w), bf16_hi(w)); }
+    static __device__ __forceinline__ Pair load(const char* base, uint32_t off) { return {*reinterpret_cast<const u32_a2*>(base + off)}; }
+    __device__ __forceinline__ float2 get() const { return make_float2(bf16_lo(w), bf16_hi(w)); }
 };
 template <>
 struct Pair<float> {
     f32x2_t w;
-    static __device__ __forceinline__ Pair load(const float* base, uint32_t off) { return {*reinterpret_cast<const f32x2_a4*>(base + off)}; }
-    __device__ __forceinline__ float2 get(bool odd) const { return make_float2(odd ? w[1] : w[0], w[1]); }
+    static __device__ __forceinline__ Pair load(const char* base, uint32_t off) { return {*reinterpret_cast<const f32x2_a4*>(base + off)}; }
+    __device__ __forceinline__ float2 get() const { return make_float2(w[0], w[1]); }
 };
 
 __device__ __forceinline__ float value_of(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
@@ -109,14 +108,16 @@ __device__ __forceinline__ void store_value(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_value(uint16_t* p, float v) { *p = (uint16_t)pack_bf16x2(v, v); }
 
 // Stores a pair, or the first of it where it has no partner.
-__device__ __forceinline__ void store_pair(uint16_t* p, float2 v, bool ok0, bool ok1) {
-    const uint32_t w = pack_bf16x2(v.x, v.y);
-    if (ok1) __builtin_nontemporal_store(w, reinterpret_cast<u32_a2*>(p));
-    else if (ok0) *p = (uint16_t)w;
-}
-__device__ __forceinline__ void store_pair(float* p, float2 v, bool ok0, bool ok1) {
-    if (ok1) __builtin_nontemporal_store(f32x2_t{v.x, v.y}, reinterpret_cast<f32x2_a4*>(p));
-    else if (ok0) *p = v.x;
+template <class T>
+__device__ __forceinline__ void store_pair(char* base, uint32_t off, float2 v, bool ok0, bool ok1) {
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t w = pack_bf16x2(v.x, v.y);
+        if (ok1) __builtin_nontemporal_store(w, reinterpret_cast<u32_a2*>(base + off));
+        else if (ok0) *reinterpret_cast<uint16_t*>(base + off) = (uint16_t)w;
+    } else {
+        if (ok1) __builtin_nontemporal_store(f32x2_t{v.x, v.y}, reinterpret_cast<f32x2_a4*>(base + off));
+        else if (ok0) *reinterpret_cast<float*>(base + off) = v.x;
+    }
 }
 
 // ------------------------------------------------- sums over lane groups ---

@@ -11,8 +11,6 @@
 // end.  Sums over states (du, ddt, dz) are in the lane but for steps over the lane groups, which four tokens share;
 // sums over channels (db, dc) go through LDS: each token's eight values of a lane are summed eight lanes at a time, then over the
 // workgroup's waves, and the workgroups' parts are added by a last launch, in a fixed order.
-#include <type_traits>
-
 #include "ssm_lay.hpp"
 
 namespace lrs {
@@ -30,22 +28,22 @@ template <class T, int NG, bool GATE, bool SUM>
 __device__ __forceinline__ void load_chunk(const SsmArgs& a, const Place& p, int chunk, Chunk<T, NG>& v) {
     const int64_t row0 = (int64_t)p.b * a.length + chunk * SSM_TOK;
     const int left = a.length - chunk * SSM_TOK, g = fresh_lane() / Lay<NG>::J;
-    const T *u = rows_at<T>(a.u, row0, a.u_stride), *dt = rows_at<T>(a.dt, row0, a.dt_stride), *z = rows_at<T>(a.z, row0, a.z_stride),
+    const char *u = rows_at<T>(a.u, row0, a.u_stride), *dt = rows_at<T>(a.dt, row0, a.dt_stride), *z = rows_at<T>(a.z, row0, a.z_stride),
             *dy = rows_at<T>(a.dy, row0, a.dy_stride);
 #pragma unroll
     for (int q = 0; q < Lay<NG>::Q; ++q) {
         const int r = min(q * NG + g, left - 1);
-        if (!SUM) v.u[q] = Pair<T>::load(u, row_off(r, a.u_stride, p.i));
-        v.dt[q] = Pair<T>::load(dt, row_off(r, a.dt_stride, p.i));
-        v.dy[q] = Pair<T>::load(dy, row_off(r, a.dy_stride, p.i));
-        if (GATE) v.z[q] = Pair<T>::load(z, row_off(r, a.z_stride, p.i));
+        if (!SUM) v.u[q] = Pair<T>::load(u, row_off<T>(r, a.u_stride, p.i));
+        v.dt[q] = Pair<T>::load(dt, row_off<T>(r, a.dt_stride, p.i));
+        v.dy[q] = Pair<T>::load(dy, row_off<T>(r, a.dy_stride, p.i));
+        if (GATE) v.z[q] = Pair<T>::load(z, row_off<T>(r, a.z_stride, p.i));
     }
     if (!SUM) load_group<T, NG>(a.b, a.b_stride, row0, left, p.gr, a.n, v.b);
     load_group<T, NG>(a.c, a.c_stride, row0, left, p.gr, a.n, v.c);
     if (!SUM) {
-        const float* at = a.saved + ((int64_t)p.b * a.plan.chunks + chunk) * a.n * a.d;
+        const char* at = reinterpret_cast<const char*>(a.saved + ((int64_t)p.b * a.plan.chunks + chunk) * a.n * a.d);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) v.h[s] = Pair<float>::load(at, (uint32_t)(min(4 * g + s, a.n - 1) * a.d) + (uint32_t)p.i);
+        for (int s = 0; s < 4; ++s) v.h[s] = Pair<float>::load(at, state_off(a, min(4 * g + s, a.n - 1), p.i));
     }
 }
 
@@ -77,26 +75,33 @@ __global__ __launch_bounds__(256) void ssm_rev_kernel(const SsmArgs a) {
     Chunk<T, NG> v;
     if (first < last) load_chunk<T, NG, GATE, true>(a, p, last - 1, v);
     for (int chunk = last - 1; chunk >= first; --chunk) {
-        const int lane = fresh_lane(), g = lane / J, j = lane % J;
+        const uint32_t lane = fresh_lane();
+        const int g = lane / J, j = lane % J;
         const int t0 = chunk * SSM_TOK, live = len - t0;
         const uint32_t resets = resets_of(a, b, t0, len);
         anew |= resets != 0;
+        const auto stage = [&](auto mask, auto soft) {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            const float2 x = v.dt[q].get(p.odd);
-            float2 e = v.dy[q].get(p.odd);
-            float slope, s0 = x.x + bias.x, s1 = x.y + bias.y;
-            if (a.softplus) s0 = softplus_of(s0, &slope), s1 = softplus_of(s1, &slope);
-            if (GATE) {
-                const float2 z = v.z[q].get(p.odd);
-                e.x *= z.x * sigmoid_of(z.x), e.y *= z.y * sigmoid_of(z.y);
+            for (int q = 0; q < Q; ++q) {
+                const float2 x = own(v.dt[q].get(), p);
+                float2 e = own(v.dy[q].get(), p);
+                float slope, s0 = x.x + bias.x, s1 = x.y + bias.y;
+                if (decltype(soft)::value) s0 = softplus_of(s0, &slope), s1 = softplus_of(s1, &slope);
+                if (GATE) {
+                    const float2 z = own(v.z[q].get(), p);
+                    e.x *= z.x * sigmoid_of(z.x), e.y *= z.y * sigmoid_of(z.y);
+                }
+                if (decltype(mask)::value) {  // padding may hold anything
+                    const bool on = q * NG + g < live;
+                    s0 = on ? s0 : 0.0f, s1 = on ? s1 : 0.0f;
+                    e.x = on ? e.x : 0.0f, e.y = on ? e.y : 0.0f;
+                }
+                m.se[q * 64 + lane] = make_float4(s0, e.x, s1, e.y);
+                total.x += s0, total.y += s1;
             }
-            const bool on = q * NG + g < live, on0 = on && p.ok0, on1 = on && p.ok1;
-            const float4 w = make_float4(on0 ? s0 : 0.0f, on0 ? e.x : 0.0f, on1 ? s1 : 0.0f, on1 ? e.y : 0.0f);
-            m.se[q * 64 + lane] = w;
-            total.x += w.x, total.y += w.z;
-        }
-        put_group<T, NG>(v.c, m.c, live, a.n);
+            put_group<decltype(mask)::value, T, NG>(v.c, m.c, live, a.n);
+        };
+        both_ways(!whole_chunk<NG>(a, p.tile, live), [&](auto mask) { both_ways(a.softplus, [&](auto soft) { stage(mask, soft); }); });
         if (chunk > first) load_chunk<T, NG, GATE, true>(a, p, chunk - 1, v);
         wave_lds_sync();
         const auto walk = [&](auto starts) {
@@ -116,8 +121,7 @@ __global__ __launch_bounds__(256) void ssm_rev_kernel(const SsmArgs a) {
                 if (t % 2 == 0) __builtin_amdgcn_sched_barrier(0);
             }
         };
-        if (resets) walk(std::true_type{});
-        else walk(std::false_type{});
+        both_ways(resets != 0, walk);
         wave_lds_sync();
     }
     put_segment<NG>(a, p, A, okn, total, anew, G);
@@ -129,12 +133,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const SsmArgs a)
     using Y = Lay<NG>;
     constexpr int Q = Y::Q, J = Y::J, N4 = Y::N4, ROW = 68;  // a row of 64 lanes' values, padded
     constexpr int PART = NG == 16 ? 16 : 8, QP = PART / NG;   // tokens whose states are in registers at once
+    // dy (z sigmoid(z))' of a token's channels, and once that is used, the sums of its dc and db over the wave's channels
+    constexpr int PITCH = 2 * J > 8 * NG ? 2 * J : 8 * NG;
     struct Wave {
         float4 su[SSM_TOK * J];                                // s, s u of two channels
-        float2 e[SSM_TOK * J], slope[SSM_TOK * J], gate[SSM_TOK * J], u[SSM_TOK * J];  // e; softplus'; dy (z sigmoid(z))'; u
+        float2 e[SSM_TOK * J], slope[SSM_TOK * J], u[SSM_TOK * J];  // e; softplus'; u
+        float gate[SSM_TOK][PITCH];
         float4 b[SSM_TOK * NG], c[SSM_TOK * NG];
-        float in[8 * ROW];                                     // a token's values of dc, db by lane
-        float sum[SSM_TOK][8 * NG];                            // their sums over the wave's channels
+        float in[2][8 * ROW];                                  // a token's values of dc, db by lane
     };
     __shared__ Wave waves[WAVES];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -156,45 +162,57 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const SsmArgs a)
             if (!(c ? p.ok1 : p.ok0) || !okn[s]) continue;
             const int n = 4 * p.g + s;
             if (a.dh) G[c][s] = a.dh[((int64_t)b * a.d + p.c0 + c) * a.n + n];
-            G[c][s] = through_segments(a, p, c, n, segs - 1, seg, -1, G[c][s]);  // what those behind this one hand on
         }
+    through_segments(a, p, segs - 1, seg, -1, G);  // what those behind this one hand on
+#pragma unroll
+    for (int s = 0; s < 4; ++s) G[0][s] = p.ok0 && okn[s] ? G[0][s] : 0.0f, G[1][s] = p.ok1 && okn[s] ? G[1][s] : 0.0f;
     const float2 bias = load_two(a.dt_bias, p), skip = load_two(a.skip, p);
     float2 dskip = make_float2(0.f, 0.f), dbias = make_float2(0.f, 0.f);
     const int first = seg * a.plan.seg, last = min(first + a.plan.seg, a.plan.chunks);
     Chunk<T, NG> v;
     if (first < last) load_chunk<T, NG, GATE, false>(a, p, last - 1, v);
     for (int chunk = last - 1; chunk >= first; --chunk) {
-        const int lane = fresh_lane(), g = lane / J, j = lane % J;
+        const uint32_t lane = fresh_lane();
+        const int g = lane / J, j = lane % J;
         const int t0 = chunk * SSM_TOK, live = len - t0, left = a.length - t0;
         const int64_t row0 = (int64_t)b * a.length + t0;
         const uint32_t resets = resets_of(a, b, t0, len);
         float hin[2][4];
+        const auto stage = [&](auto mask, auto soft) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const float2 x = v.h[s].get(p.odd);
-            hin[0][s] = p.ok0 && okn[s] ? x.x : 0.0f, hin[1][s] = p.ok1 && okn[s] ? x.y : 0.0f;
-        }
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            const int at = q * 64 + lane;
-            const bool on = q * NG + g < live, on0 = on && p.ok0, on1 = on && p.ok1;
-            const float2 x = v.dt[q].get(p.odd), dy = v.dy[q].get(p.odd);
-            float2 u = v.u[q].get(p.odd), e = dy, slope = make_float2(1.f, 1.f), s = make_float2(x.x + bias.x, x.y + bias.y);
-            if (a.softplus) s.x = softplus_of(s.x, &slope.x), s.y = softplus_of(s.y, &slope.y);
-            if (GATE) {
-                const float2 z = v.z[q].get(p.odd);
-                const float g0 = sigmoid_of(z.x), g1 = sigmoid_of(z.y);
-                e.x *= z.x * g0, e.y *= z.y * g1;
-                m.gate[at] = make_float2(dy.x * (g0 * (1.0f + z.x * (1.0f - g0))), dy.y * (g1 * (1.0f + z.y * (1.0f - g1))));
+            for (int s = 0; s < 4; ++s) {
+                const float2 x = own(v.h[s].get(), p);
+                const bool on = !decltype(mask)::value || okn[s];
+                hin[0][s] = on ? x.x : 0.0f, hin[1][s] = on ? x.y : 0.0f;
             }
-            u.x = on0 ? u.x : 0.0f, u.y = on1 ? u.y : 0.0f;  // padding may hold anything
-            m.u[at] = u;
-            m.su[at] = make_float4(on0 ? s.x : 0.0f, on0 ? s.x * u.x : 0.0f, on1 ? s.y : 0.0f, on1 ? s.y * u.y : 0.0f);
-            m.e[at] = make_float2(on0 ? e.x : 0.0f, on1 ? e.y : 0.0f);
-            m.slope[at] = slope;
-        }
-        put_group<T, NG>(v.b, m.b, live, a.n);
-        put_group<T, NG>(v.c, m.c, live, a.n);
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const uint32_t at = q * 64 + lane;
+                const float2 x = own(v.dt[q].get(), p), dy = own(v.dy[q].get(), p);
+                float2 u = own(v.u[q].get(), p), slope = make_float2(1.f, 1.f), s = make_float2(x.x + bias.x, x.y + bias.y), e = dy;
+                if (decltype(soft)::value) s.x = softplus_of(s.x, &slope.x), s.y = softplus_of(s.y, &slope.y);
+                if (GATE) {
+                    const float2 z = own(v.z[q].get(), p);
+                    const float g0 = sigmoid_of(z.x), g1 = sigmoid_of(z.y), s0 = z.x * g0, s1 = z.y * g1;
+                    e.x *= s0, e.y *= s1;
+                    // (z sigmoid(z))' = sigmoid(z) + z sigmoid(z) (1 - sigmoid(z))
+                    reinterpret_cast<float2*>(m.gate[q * NG + g])[j] = make_float2(dy.x * fmaf(s0, 1.0f - g0, g0), dy.y * fmaf(s1, 1.0f - g1, g1));
+                }
+                if (decltype(mask)::value) {  // padding may hold anything, and channels that do not exist add nothing to db and dc
+                    const bool on = q * NG + g < live, on0 = on && p.ok0, on1 = on && p.ok1;
+                    s.x = on ? s.x : 0.0f, s.y = on ? s.y : 0.0f;
+                    u.x = on0 ? u.x : 0.0f, u.y = on1 ? u.y : 0.0f;
+                    e.x = on0 ? e.x : 0.0f, e.y = on1 ? e.y : 0.0f;
+                }
+                m.u[at] = u;
+                m.su[at] = make_float4(s.x, s.x * u.x, s.y, s.y * u.y);
+                m.e[at] = e;
+                m.slope[at] = slope;
+            }
+            put_group<decltype(mask)::value, T, NG>(v.b, m.b, live, a.n);
+            put_group<decltype(mask)::value, T, NG>(v.c, m.c, live, a.n);
+        };
+        both_ways(!whole_chunk<NG>(a, p.tile, live), [&](auto mask) { both_ways(a.softplus, [&](auto soft) { stage(mask, soft); }); });
         if (chunk > first) load_chunk<T, NG, GATE, false>(a, p, chunk - 1, v);
         wave_lds_sync();
 
@@ -247,11 +265,27 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const SsmArgs a)
                         const int r = p0 + q * NG + g, at = (p0 / NG + q) * 64 + lane;
                         const bool on = r < live;
                         const float r0 = group_sum<NG>(y0), r1 = group_sum<NG>(y1);
-                        const float2 w = m.gate[at], u = m.u[at];
+                        const float2 w = reinterpret_cast<const float2*>(m.gate[r])[j], u = m.u[at];
                         const float2 dz = make_float2(on ? w.x * fmaf(skip.x, u.x, r0) : 0.0f, on ? w.y * fmaf(skip.y, u.y, r1) : 0.0f);
-                        store_pair(rows_at<T>(a.dz, row0, a.d) + row_off(r, a.d, p.c0), dz, r < left && p.ok0, r < left && p.ok1);
+                        store_pair<T>(rows_at<T>(a.dz, row0, a.d), row_off<T>(r, a.d, p.c0), dz, r < left && p.ok0, r < left && p.ok1);
                     }
                 }
+                // dc and db of token t: lane r sums value r / 8 of lanes 8 (r % 8) and the seven behind it
+                const auto sum_up = [&](int t) {
+                    const float4* in = reinterpret_cast<const float4*>(m.in[t % 2] + (lane >> 3) * ROW + (lane & 7) * 8);
+                    const float4 lo = in[0], hi = in[1];
+                    float* to = m.gate[t] + (lane >> 3) * NG;
+                    const float l = (lo.x + lo.y) + (lo.z + lo.w), u = (hi.x + hi.y) + (hi.z + hi.w);
+                    if constexpr (NG == 16) {
+                        to[2 * (lane & 7)] = l, to[2 * (lane & 7) + 1] = u;
+                    } else {
+                        float w = l + u;
+                        if constexpr (NG <= 4) w += row_xor<1>(w);
+                        if constexpr (NG <= 2) w += row_xor<2>(w);
+                        if constexpr (NG <= 1) w += row_xor<4>(w);
+                        if ((lane & 7) % (8 / NG) == 0) to[(lane & 7) * NG / 8] = w;
+                    }
+                };
 #pragma unroll
                 for (int q = QP - 1; q >= 0; --q) {
                     float gb0[NG], gb1[NG], ar0[NG], ar1[NG];
@@ -262,7 +296,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const SsmArgs a)
                         const float2 e = m.e[t * J + j];
                         const float bs[4] = {B.x, B.y, B.z, B.w}, cs[4] = {C.x, C.y, C.z, C.w};
                         const bool start = begins(t);
-                        float* in = m.in + lane;
+                        float* in = m.in[t % 2] + lane;
+                        // what the token behind this one left, while this one's is formed
+                        if (k < PART - 1) sum_up(t + 1);
                         gb0[i] = gb1[i] = ar0[i] = ar1[i] = 0.0f;
 #pragma unroll
                         for (int s = 0; s < 4; ++s) {
@@ -280,21 +316,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const SsmArgs a)
                             asm volatile("" : "+v"(dA[0][s]), "+v"(dA[1][s]));
                         }
                         wave_lds_sync();
-                        // lane r sums value r / 8 of lanes 8 (r % 8) and the seven behind it
-                        const float4* in8 = reinterpret_cast<const float4*>(m.in + (lane >> 3) * ROW + (lane & 7) * 8);
-                        const float4 lo = in8[0], hi = in8[1];
-                        float* to = m.sum[t] + (lane >> 3) * NG;
-                        const float l = (lo.x + lo.y) + (lo.z + lo.w), u = (hi.x + hi.y) + (hi.z + hi.w);
-                        if constexpr (NG == 16) {
-                            to[2 * (lane & 7)] = l, to[2 * (lane & 7) + 1] = u;
-                        } else {
-                            float w = l + u;
-                            if constexpr (NG <= 4) w += row_xor<1>(w);
-                            if constexpr (NG <= 2) w += row_xor<2>(w);
-                            if constexpr (NG <= 1) w += row_xor<4>(w);
-                            if ((lane & 7) % (8 / NG) == 0) to[(lane & 7) * NG / 8] = w;
-                        }
-                        wave_lds_sync();
                     }
                     const int r = p0 + q * NG + g, at = (p0 / NG + q) * 64 + lane;
                     const float sb0 = group_sum<NG>(gb0), sb1 = group_sum<NG>(gb1);
@@ -306,22 +327,23 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const SsmArgs a)
                     const float2 dd = make_float2(on ? fmaf(u.x, sb0, sa0) * slope.x : 0.0f, on ? fmaf(u.y, sb1, sa1) * slope.y : 0.0f);
                     dskip.x = fmaf(e.x, u.x, dskip.x), dskip.y = fmaf(e.y, u.y, dskip.y);
                     dbias.x += dd.x, dbias.y += dd.y;
-                    const uint32_t off = row_off(r, a.d, p.c0);
-                    store_pair(rows_at<T>(a.du, row0, a.d) + off, du, in0, in1);
-                    store_pair(rows_at<T>(a.ddt, row0, a.d) + off, dd, in0, in1);
+                    const uint32_t off = row_off<T>(r, a.d, p.c0);
+                    store_pair<T>(rows_at<T>(a.du, row0, a.d), off, du, in0, in1);
+                    store_pair<T>(rows_at<T>(a.ddt, row0, a.d), off, dd, in0, in1);
                 }
+                sum_up(p0);
+                wave_lds_sync();
             };
             if constexpr (PART < SSM_TOK) part(PART, mid);
             part(0, hin);
         };
-        if (resets) walk(std::true_type{});
-        else walk(std::false_type{});
+        both_ways(resets != 0, walk);
         __syncthreads();
         for (int x = threadIdx.x; x < SSM_TOK * 8 * NG; x += 64 * WAVES) {
             const int n = x % N4, k = x / N4 % 2, t = x / (2 * N4), at = (k * 4 + n % 4) * NG + n / 4;
-            float w = waves[0].sum[t][at];
+            float w = waves[0].gate[t][at];
 #pragma unroll
-            for (int i = 1; i < WAVES; ++i) w += waves[i].sum[t][at];
+            for (int i = 1; i < WAVES; ++i) w += waves[i].gate[t][at];
             if (t0 + t < a.length) a.part_bc[(((int64_t)block * a.batch + b) * a.length + t0 + t) * 2 * N4 + k * N4 + n] = w;
         }
         __syncthreads();
@@ -334,19 +356,19 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const SsmArgs a)
                 if ((c ? p.ok1 : p.ok0) && okn[s]) a.dh0[((int64_t)b * a.d + p.c0 + c) * a.n + 4 * p.g + s] = G[c][s];
     }
     const int64_t mine = (int64_t)b * segs + seg;
-    float* at = a.part_a + (mine * a.n + 4 * p.g) * a.d + p.c0;
+    char* at = reinterpret_cast<char*>(a.part_a + mine * a.n * a.d);
 #pragma unroll
-    for (int s = 0; s < 4; ++s, at += a.d)
-        if (okn[s]) store_pair(at, make_float2(dA[0][s], dA[1][s]), p.ok0, p.ok1);
+    for (int s = 0; s < 4; ++s)
+        if (okn[s]) store_pair<float>(at, state_off(a, 4 * p.g + s, p.c0), make_float2(dA[0][s], dA[1][s]), p.ok0, p.ok1);
 #pragma unroll
     for (int o = 32; o >= J; o >>= 1) {
         dskip.x += __shfl_xor(dskip.x, o), dskip.y += __shfl_xor(dskip.y, o);
         dbias.x += __shfl_xor(dbias.x, o), dbias.y += __shfl_xor(dbias.y, o);
     }
     if (p.g == 0) {
-        float* pd = a.part_d + mine * 2 * a.d + p.c0;
-        store_pair(pd, dskip, p.ok0, p.ok1);
-        store_pair(pd + a.d, dbias, p.ok0, p.ok1);
+        char* pd = reinterpret_cast<char*>(a.part_d + mine * 2 * a.d);
+        store_pair<float>(pd, state_off(a, 0, p.c0), dskip, p.ok0, p.ok1);
+        store_pair<float>(pd, state_off(a, 1, p.c0), dbias, p.ok0, p.ok1);
     }
 }
 

@@ -10,8 +10,6 @@
 // through LDS to the lanes that hold the states.  A wave holds two channels by four states a lane: of 16 states its lanes are four
 // groups of states of 16 channel pairs, so that a value from LDS serves four or eight states and the sum over states is
 // in the lane but for two steps, which are taken for four tokens at once.
-#include <type_traits>
-
 #include "ssm_lay.hpp"
 
 namespace lrs {
@@ -28,13 +26,13 @@ template <class T, int NG, bool GATE, bool SUM>
 __device__ __forceinline__ void load_chunk(const SsmArgs& a, const Place& p, int chunk, Chunk<T, NG>& v) {
     const int64_t row0 = (int64_t)p.b * a.length + chunk * SSM_TOK;
     const int left = a.length - chunk * SSM_TOK, g = fresh_lane() / Lay<NG>::J;
-    const T *u = rows_at<T>(a.u, row0, a.u_stride), *dt = rows_at<T>(a.dt, row0, a.dt_stride), *z = rows_at<T>(a.z, row0, a.z_stride);
+    const char *u = rows_at<T>(a.u, row0, a.u_stride), *dt = rows_at<T>(a.dt, row0, a.dt_stride), *z = rows_at<T>(a.z, row0, a.z_stride);
 #pragma unroll
     for (int q = 0; q < Lay<NG>::Q; ++q) {
         const int r = min(q * NG + g, left - 1);
-        v.u[q] = Pair<T>::load(u, row_off(r, a.u_stride, p.i));
-        v.dt[q] = Pair<T>::load(dt, row_off(r, a.dt_stride, p.i));
-        if (!SUM && GATE) v.z[q] = Pair<T>::load(z, row_off(r, a.z_stride, p.i));
+        v.u[q] = Pair<T>::load(u, row_off<T>(r, a.u_stride, p.i));
+        v.dt[q] = Pair<T>::load(dt, row_off<T>(r, a.dt_stride, p.i));
+        if (!SUM && GATE) v.z[q] = Pair<T>::load(z, row_off<T>(r, a.z_stride, p.i));
     }
     load_group<T, NG>(a.b, a.b_stride, row0, left, p.gr, a.n, v.b);
     if (!SUM) load_group<T, NG>(a.c, a.c_stride, row0, left, p.gr, a.n, v.c);
@@ -70,8 +68,10 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(const SsmArgs a) {
             if (SUM || !(c ? p.ok1 : p.ok0) || !okn[s]) continue;
             const int n = 4 * p.g + s;
             if (a.h0) h[c][s] = a.h0[((int64_t)b * a.d + p.c0 + c) * a.n + n];
-            h[c][s] = through_segments(a, p, c, n, 0, seg, 1, h[c][s]);  // what those before this one leave
         }
+    if (!SUM) through_segments(a, p, 0, seg, 1, h);  // what those before this one leave
+#pragma unroll
+    for (int s = 0; s < 4; ++s) h[0][s] = p.ok0 && okn[s] ? h[0][s] : 0.0f, h[1][s] = p.ok1 && okn[s] ? h[1][s] : 0.0f;
     const float2 bias = load_two(a.dt_bias, p), skip = load_two(SUM ? nullptr : a.skip, p);
     float2 total = make_float2(0.f, 0.f);
     bool anew = false;
@@ -79,38 +79,46 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(const SsmArgs a) {
     Chunk<T, NG> v;
     if (first < last) load_chunk<T, NG, GATE, SUM>(a, p, first, v);
     for (int chunk = first; chunk < last; ++chunk) {
-        const int lane = fresh_lane(), g = lane / J, j = lane % J;
+        const uint32_t lane = fresh_lane();
+        const int g = lane / J, j = lane % J;
         const int t0 = chunk * SSM_TOK, live = len - t0, left = a.length - t0;
         if (!SUM && a.saved) {
-            float* at = a.saved + ((int64_t)b * a.plan.chunks + chunk) * a.n * a.d;
+            char* at = reinterpret_cast<char*>(a.saved + ((int64_t)b * a.plan.chunks + chunk) * a.n * a.d);
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-                if (okn[s]) store_pair(at + ((uint32_t)((4 * g + s) * a.d) + (uint32_t)p.c0), make_float2(h[0][s], h[1][s]), p.ok0, p.ok1);
+                if (okn[s]) store_pair<float>(at, state_off(a, 4 * g + s, p.c0), make_float2(h[0][s], h[1][s]), p.ok0, p.ok1);
         }
         const uint32_t resets = resets_of(a, b, t0, len);
         anew |= resets != 0;
         float2 us[Q], gate[Q];
+        const auto stage = [&](auto mask, auto soft) {
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            const float2 u = v.u[q].get(p.odd), x = v.dt[q].get(p.odd);
-            float slope, s0 = x.x + bias.x, s1 = x.y + bias.y;
-            if (a.softplus) s0 = softplus_of(s0, &slope), s1 = softplus_of(s1, &slope);
-            const bool on = q * NG + g < live, on0 = on && p.ok0, on1 = on && p.ok1;
-            const float4 w = make_float4(on0 ? s0 : 0.0f, on0 ? s0 * u.x : 0.0f, on1 ? s1 : 0.0f, on1 ? s1 * u.y : 0.0f);
-            m.su[q * 64 + lane] = w;
-            if (SUM) {
-                total.x += w.x, total.y += w.z;
-            } else {
-                us[q] = u;
-                gate[q] = make_float2(1.0f, 1.0f);
-                if (GATE) {
-                    const float2 z = v.z[q].get(p.odd);
-                    gate[q] = make_float2(z.x * sigmoid_of(z.x), z.y * sigmoid_of(z.y));
+            for (int q = 0; q < Q; ++q) {
+                float2 u = own(v.u[q].get(), p);
+                const float2 x = own(v.dt[q].get(), p);
+                float slope, s0 = x.x + bias.x, s1 = x.y + bias.y;
+                if (decltype(soft)::value) s0 = softplus_of(s0, &slope), s1 = softplus_of(s1, &slope);
+                if (decltype(mask)::value) {  // padding may hold anything
+                    const bool on = q * NG + g < live;
+                    s0 = on ? s0 : 0.0f, s1 = on ? s1 : 0.0f;
+                    u.x = on ? u.x : 0.0f, u.y = on ? u.y : 0.0f;
+                }
+                m.su[q * 64 + lane] = make_float4(s0, s0 * u.x, s1, s1 * u.y);
+                if (SUM) {
+                    total.x += s0, total.y += s1;
+                } else {
+                    us[q] = u;
+                    gate[q] = make_float2(1.0f, 1.0f);
+                    if (GATE) {
+                        const float2 z = own(v.z[q].get(), p);
+                        gate[q] = make_float2(z.x * sigmoid_of(z.x), z.y * sigmoid_of(z.y));
+                    }
                 }
             }
-        }
-        put_group<T, NG>(v.b, m.b, live, a.n);
-        if (!SUM) put_group<T, NG>(v.c, m.c, live, a.n);
+            put_group<decltype(mask)::value, T, NG>(v.b, m.b, live, a.n);
+            if (!SUM) put_group<decltype(mask)::value, T, NG>(v.c, m.c, live, a.n);
+        };
+        both_ways(!whole_chunk<NG>(a, p.tile, live), [&](auto mask) { both_ways(a.softplus, [&](auto soft) { stage(mask, soft); }); });
         if (chunk + 1 < last) load_chunk<T, NG, GATE, SUM>(a, p, chunk + 1, v);
         wave_lds_sync();
         // a chunk without a sequence's start, as most are, runs free of branches
@@ -144,12 +152,11 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(const SsmArgs a) {
                     const float r0 = group_sum<NG>(y0), r1 = group_sum<NG>(y1);
                     const bool on = r < live;  // padding: whatever u and z hold
                     const float2 y = make_float2(on ? fmaf(skip.x, us[q].x, r0) * gate[q].x : 0.0f, on ? fmaf(skip.y, us[q].y, r1) * gate[q].y : 0.0f);
-                    store_pair(rows_at<T>(a.y, (int64_t)b * a.length + t0, a.d) + row_off(r, a.d, p.c0), y, r < left && p.ok0, r < left && p.ok1);
+                    store_pair<T>(rows_at<T>(a.y, (int64_t)b * a.length + t0, a.d), row_off<T>(r, a.d, p.c0), y, r < left && p.ok0, r < left && p.ok1);
                 }
             }
         };
-        if (resets) walk(std::true_type{});
-        else walk(std::false_type{});
+        both_ways(resets != 0, walk);
         wave_lds_sync();
     }
     if (SUM) {

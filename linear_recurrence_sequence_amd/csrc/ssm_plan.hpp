@@ -44,7 +44,7 @@ inline SsmPlan ssm_plan(int64_t batch, int64_t length, int d, int n, int groups,
     p.chunks = (int)ceil_div(length, SSM_TOK);
     const int64_t want = backward ? 2048 : 4096;
     const int64_t units = std::max<int64_t>(1, batch * groups * (backward ? (int64_t)p.blocks * p.waves : p.tiles));
-    const int64_t s = std::min<int64_t>({ceil_div(want, units), 64, std::max(1, p.chunks)});
+    const int64_t s = std::max<int64_t>(1, std::min<int64_t>({want / units, 64, p.chunks}));
     p.seg = (int)ceil_div(std::max(1, p.chunks), s);
     p.segments = (int)ceil_div(std::max(1, p.chunks), p.seg);
     return p;
