@@ -142,7 +142,7 @@ scan_status lm_adamw_step(int count, int param_dtype, int grad_dtype, int state_
  * vocabulary's rows w [v, d].  A negative token is padding: its row of out is
  * zero, and it has no gradient.  A token >= v: its row is NaN, without one either.
  * Products are FP32, out is rounded once (where it is BF16).
- * 1 <= d <= 2^24, v >= 1, 0 <= n < 2^27, v + n / 16 < 2^26 - 32, n ceil(d / 4) < 2^32 - 256.
+ * 1 <= d <= 2^23, 1 <= v < 2^31 - 256, 0 <= n <= 2^26 - 64.
  * ====================================================================== */
 
 /* Forward.  w [v, d] of w_dtype and out [n, d] of out_dtype, dense. */

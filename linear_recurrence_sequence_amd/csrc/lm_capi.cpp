@@ -79,14 +79,13 @@ scan_status ce_check(const char* fn, int64_t n, int d, int64_t v, double cap, in
     return SCAN_OK;
 }
 
-// Launches of a thread for four columns of a token, 64 for a row of the vocabulary, 32 for a token.
+// Launches of up to 64 threads for a token or a row of the vocabulary along x, and a workgroup for 256 columns along y.
 bool embed_shape(int64_t n, int d, int64_t v) {
-    return n >= 0 && d >= 1 && v >= 1 && n <= (MOST_THREADS - 1024) / 32 && v <= (MOST_THREADS - 1024) / 64 - n / 16 - 8 && d <= (1 << 24) &&
-           (__int128)n * ceil_div(d, 4) <= MOST_THREADS - 256;
+    return n >= 0 && d >= 1 && v >= 1 && n <= (1 << 26) - 64 && v <= 0x7fffff00 && d <= (1 << 23);
 }
 scan_status embed_refuse(const char* fn, int64_t n, int d, int64_t v) {
     return fail(SCAN_ERR_SHAPE, std::string(fn) + ": unsupported shape n=" + std::to_string(n) + " d=" + std::to_string(d) + " v=" +
-                                    std::to_string(v) + " (need 1 <= d <= 2^24, v >= 1, n < 2^27, v + n / 16 < 2^26 - 32, n ceil(d / 4) < 2^32 - 256)");
+                                    std::to_string(v) + " (need 1 <= d <= 2^23, 1 <= v < 2^31 - 256, n <= 2^26 - 64)");
 }
 
 // The gradient's buffers inside the caller's workspace (base NULL: sizes only).

@@ -17,23 +17,30 @@ namespace {
 
 constexpr int WAVES = 16;  // of a sorting workgroup
 
-// quads: groups of four columns; a thread has one of a token's.
+constexpr int BATCH = 4;   // groups of 256 columns (and tokens, in the gradient) whose loads of a wave are in flight together
+
+// A wave takes BATCH * 256 columns of a token.
 template <class WT, class OT, bool TAIL>
 __global__ __launch_bounds__(256) void embed_fwd_kernel(const EmbedArgs a) {
-    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x, quads = (a.d + 3) / 4, t = x / quads;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = (int64_t)blockIdx.x * 4 + wave;
     if (t >= a.n) return;
-    const int col = 4 * (int)(x % quads);
+    const int c0 = blockIdx.y * (256 * BATCH) + 4 * lane;
     const int64_t tok = a.tokens[t];
-    float v[4];
-    if (tok >= 0 && tok < a.v) {
-        take<TAIL>(row_load<WT, TAIL>(static_cast<const WT*>(a.w) + tok * a.d, col, a.d), col, a.d, v);
+    const bool on = tok >= 0 && tok < a.v;
+    const WT* row = static_cast<const WT*>(a.w) + (on ? tok : 0) * a.d;
+    Quad<WT> q[BATCH];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] *= a.scale;
-    } else {
+    for (int c = 0; c < BATCH; ++c) q[c] = row_load<WT, TAIL>(row, min(c0 + 256 * c, a.d - 1), a.d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = tok < 0 ? 0.0f : __builtin_nanf("");
+    for (int c = 0; c < BATCH; ++c) {
+        const int col = c0 + 256 * c;
+        float v[4];
+        take<TAIL>(q[c], col, a.d, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = on ? v[i] * a.scale : tok < 0 ? 0.0f : __builtin_nanf("");
+        row_store<OT, TAIL>(static_cast<OT*>(a.out) + t * a.d, col, a.d, v);
     }
-    row_store<OT, TAIL>(static_cast<OT*>(a.out) + t * a.d, col, a.d, v);
 }
 
 __global__ __launch_bounds__(64 * WAVES) void embed_sort_kernel(const EmbedArgs a) {
@@ -94,46 +101,60 @@ __global__ __launch_bounds__(64 * WAVES) void embed_sort_kernel(const EmbedArgs 
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             const bool here = t[u] >= lo && t[u] < hi;
-            uint64_t same = __ballot(here);
+            const uint64_t same = __ballot(here);
             if (!same) continue;
             const int key = here ? (int)(t[u] - lo) : 0;
+            uint32_t s0 = (uint32_t)same, s1 = (uint32_t)(same >> 32);
 #pragma unroll
-            for (int bit = 1; bit < EMBED_ROWS; bit <<= 1) {  // lanes with the same row
-                const uint64_t m = __ballot((key & bit) != 0);
-                same &= key & bit ? m : ~m;
+            for (int bit = 0; 1 << bit < EMBED_ROWS; ++bit) {  // lanes with the same row: those whose bits all agree
+                const uint64_t m = __ballot((key >> bit & 1) != 0);
+                const uint32_t own = (uint32_t)-(key >> bit & 1);
+                s0 &= ~((uint32_t)m ^ own), s1 &= ~((uint32_t)(m >> 32) ^ own);
             }
-            const int rank = __popcll(same & ((1ull << lane) - 1));
+            const int rank = __builtin_amdgcn_mbcnt_hi(s1, __builtin_amdgcn_mbcnt_lo(s0, 0));
             if (here) a.order[count[wave][key] + rank] = (int)(i0 + 64 * u + lane);
             wave_lds_sync();
-            if (here && rank == 0) count[wave][key] += __popcll(same);
+            if (here && rank == 0) count[wave][key] += __popc(s0) + __popc(s1);
             wave_lds_sync();
         }
     }
 }
 
-// Adds rows order[p0..p1) of dout to s, eight of them on their way at a time.
+// Adds rows order[p0..p1) of dout, at most EMBED_RUN, to s: BATCH groups of 256 columns from c0 on.
 template <class OT, bool TAIL>
-__device__ __forceinline__ void add_rows(const EmbedArgs& a, int p0, int p1, int col, float* s) {
-    for (int p = p0; p < p1; p += 8) {
-        Quad<OT> q[8];
+__device__ __forceinline__ void add_rows(const EmbedArgs& a, int p0, int p1, int c0, float (&s)[BATCH][4]) {
+    const int lane = threadIdx.x & 63, mine = a.order[min(p0 + lane, p1 - 1)];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            const int64_t t = a.order[min(p + u, p1 - 1)];
-            q[u] = row_load<OT, TAIL>(static_cast<const OT*>(a.dout) + t * a.dout_stride, col, a.d);
+    for (int c = 0; c < BATCH; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[c][i] = 0.0f;
+    for (int p = 0; p < p1 - p0; p += BATCH) {
+        Quad<OT> q[BATCH][BATCH];
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+            const int64_t t = __builtin_amdgcn_readlane(mine, min(p + u, p1 - p0 - 1));
+            const OT* row = static_cast<const OT*>(a.dout) + t * a.dout_stride;
+#pragma unroll
+            for (int c = 0; c < BATCH; ++c) {
+                const int col = c0 + 256 * c + 4 * lane;
+                q[u][c] = row_load<OT, TAIL>(row, min(col, a.d - 1), a.d);
+            }
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            float v[4];
-            take<TAIL>(q[u], col, a.d, v);
+        for (int u = 0; u < BATCH; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[i] += p + u < p1 ? v[i] : 0.0f;
-        }
+            for (int c = 0; c < BATCH; ++c) {
+                float v[4];
+                take<TAIL>(q[u][c], c0 + 256 * c + 4 * lane, a.d, v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[c][i] += p + u < p1 - p0 ? v[i] : 0.0f;
+            }
     }
 }
 
 // A row's gradient, rounded once; `add`: to what is there.
 template <class GT, bool TAIL>
-__device__ __forceinline__ void put_row(const EmbedArgs& a, int64_t row, int col, float* s) {
+__device__ __forceinline__ void put_row(const EmbedArgs& a, int64_t row, int col, const float* s) {
     GT* to = static_cast<GT*>(a.dw) + row * a.d;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (a.add) take<TAIL>(row_load<GT, TAIL>(to, col, a.d), col, a.d, v);
@@ -142,10 +163,12 @@ __device__ __forceinline__ void put_row(const EmbedArgs& a, int64_t row, int col
     row_store<GT, TAIL>(to, col, a.d, v);
 }
 
-// The first `runs` workgroups (of four) take the runs, the others the rows.
+// The first `runs` workgroups (of four) take the runs, the others rows: a wave every `waves`-th one, so that the frequent rows, which often stand
+// side by side, are not one wave's.
 template <class OT, class GT, bool TAIL>
-__global__ __launch_bounds__(256) void embed_grad_kernel(const EmbedArgs a, unsigned runs) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+__global__ __launch_bounds__(256) void embed_grad_kernel(const EmbedArgs a, unsigned runs, int waves) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    float s[BATCH][4];
     if (blockIdx.x < runs) {
         const int64_t run = (int64_t)blockIdx.x * 4 + wave;
         const int total = a.start[a.v];
@@ -154,36 +177,51 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(const EmbedArgs a, unsi
         const int64_t head = a.tokens[a.order[p0]], tail = a.tokens[a.order[p1 - 1]];
         const int hs = a.start[head], he = a.start[head + 1], ts = a.start[tail], te = a.start[tail + 1];
         float* part = a.part + run * 2 * a.d;
-        if (hs < p0 && he - hs > EMBED_RUN)
-            for (int col = 4 * lane; col < a.d; col += 256) {
-                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                add_rows<OT, TAIL>(a, p0, min(he, p1), col, s);
-                row_store<float, TAIL>(part, col, a.d, s);
+        for (int c0 = 0; c0 < a.d; c0 += 256 * BATCH) {
+            if (hs < p0 && he - hs > EMBED_RUN) {
+                add_rows<OT, TAIL>(a, p0, min(he, p1), c0, s);
+#pragma unroll
+                for (int c = 0; c < BATCH; ++c) row_store<float, TAIL>(part, c0 + 256 * c + 4 * lane, a.d, s[c]);
             }
-        if (ts >= p0 && te - ts > EMBED_RUN)
-            for (int col = 4 * lane; col < a.d; col += 256) {
-                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                add_rows<OT, TAIL>(a, ts, p1, col, s);
-                row_store<float, TAIL>(part + a.d, col, a.d, s);
+            if (ts >= p0 && te - ts > EMBED_RUN) {
+                add_rows<OT, TAIL>(a, ts, p1, c0, s);
+#pragma unroll
+                for (int c = 0; c < BATCH; ++c) row_store<float, TAIL>(part + a.d, c0 + 256 * c + 4 * lane, a.d, s[c]);
             }
+        }
         return;
     }
-    const int64_t row = (int64_t)(blockIdx.x - runs) * 4 + wave;
-    if (row >= a.v) return;
-    const int p0 = a.n > 0 ? a.start[row] : 0, p1 = a.n > 0 ? a.start[row + 1] : 0;
-    if (p1 - p0 > EMBED_RUN || (a.add && p0 == p1)) return;
-    for (int col = 4 * lane; col < a.d; col += 256) {
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        add_rows<OT, TAIL>(a, p0, p1, col, s);
-        put_row<GT, TAIL>(a, row, col, s);
+    const int first = (int)(blockIdx.x - runs) * 4 + wave;
+    for (int64_t k0 = first; k0 < a.v; k0 += (int64_t)64 * waves) {
+        // lane i: where the i-th of the next 64 rows begins and ends
+        const int64_t r = min(k0 + (int64_t)lane * waves, a.v - 1);
+        const int from = a.n > 0 ? a.start[r] : 0, to = a.n > 0 ? a.start[r + 1] : 0;
+        for (int i = 0; i < 64 && k0 + (int64_t)i * waves < a.v; ++i) {
+            const int64_t row = k0 + (int64_t)i * waves;
+            const int p0 = __builtin_amdgcn_readlane(from, i), p1 = __builtin_amdgcn_readlane(to, i);
+            if (p1 - p0 > EMBED_RUN || (a.add && p0 == p1)) continue;
+            if (p0 == p1) {
+                const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int col = 4 * lane; col < a.d; col += 256) row_store<GT, TAIL>(static_cast<GT*>(a.dw) + row * a.d, col, a.d, none);
+                continue;
+            }
+            for (int c0 = 0; c0 < a.d; c0 += 256 * BATCH) {
+                add_rows<OT, TAIL>(a, p0, p1, c0, s);
+#pragma unroll
+                for (int c = 0; c < BATCH; ++c)
+                    if (c0 + 256 * c + 4 * lane < a.d) put_row<GT, TAIL>(a, row, c0 + 256 * c + 4 * lane, s[c]);
+            }
+        }
     }
 }
 
-// Rows of more than EMBED_RUN tokens: the workgroup of the run that such a row begins in adds its parts, wave w the w-th of each 16.
+// Rows of more than EMBED_RUN tokens: the workgroups of the run that such a row begins in add its parts, wave w the w-th of each JOIN_WAVES,
+// 256 columns a workgroup.
+constexpr int JOIN_WAVES = 4;
 template <class GT, bool TAIL>
-__global__ __launch_bounds__(64 * WAVES) void embed_join_kernel(const EmbedArgs a) {
-    __shared__ float4 sum[WAVES][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+__global__ __launch_bounds__(64 * JOIN_WAVES) void embed_join_kernel(const EmbedArgs a) {
+    __shared__ float4 sum[JOIN_WAVES][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = blockIdx.y * 256 + 4 * lane;
     const int64_t run = blockIdx.x;
     const int total = a.start[a.v];
     if (run * EMBED_RUN >= total) return;
@@ -192,33 +230,35 @@ __global__ __launch_bounds__(64 * WAVES) void embed_join_kernel(const EmbedArgs 
     const int s0 = a.start[row], e0 = a.start[row + 1];
     if (s0 < p0 || e0 - s0 <= EMBED_RUN) return;
     const int parts = (e0 - 1) / EMBED_RUN - (int)run + 1;
-    for (int c0 = 0; c0 < a.d; c0 += 256) {
-        const int col = c0 + 4 * lane;
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (col < a.d)
-            for (int i = wave; i < parts; i += WAVES) {
-                float v[4];
-                const float* from = a.part + (run + i) * 2 * a.d + (i ? 0 : a.d);  // its first part is the end of a run
-                take<TAIL>(row_load<float, TAIL>(from, col, a.d), col, a.d, v);
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i0 = wave; i0 < parts; i0 += 4 * JOIN_WAVES) {
+        Quad<float> q[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) s[k] += v[k];
-            }
-        sum[wave][lane] = make_float4(s[0], s[1], s[2], s[3]);
-        __syncthreads();
-        if (wave == 0 && col < a.d) {
-            for (int w = 1; w < WAVES; ++w) {
-                const float4 v = sum[w][lane];
-                s[0] += v.x, s[1] += v.y, s[2] += v.z, s[3] += v.w;
-            }
-            put_row<GT, TAIL>(a, row, col, s);
+        for (int u = 0; u < 4; ++u) {
+            const int i = min(i0 + u * JOIN_WAVES, parts - 1);
+            q[u] = row_load<float, TAIL>(a.part + (run + i) * 2 * a.d + (i ? 0 : a.d), min(col, a.d - 1), a.d);  // its first part is the end of a run
         }
-        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            float v[4];
+            take<TAIL>(q[u], col, a.d, v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[k] += i0 + u * JOIN_WAVES < parts ? v[k] : 0.0f;
+        }
     }
+    sum[wave][lane] = make_float4(s[0], s[1], s[2], s[3]);
+    __syncthreads();
+    if (wave > 0 || col >= a.d) return;
+    for (int w = 1; w < JOIN_WAVES; ++w) {
+        const float4 v = sum[w][lane];
+        s[0] += v.x, s[1] += v.y, s[2] += v.z, s[3] += v.w;
+    }
+    put_row<GT, TAIL>(a, row, col, s);
 }
 
 template <class WT, class OT>
 void launch_fwd(const EmbedArgs& a, hipStream_t s) {
-    const dim3 g((unsigned)ceil_div(a.n * ceil_div(a.d, 4), 256)), b(256);
+    const dim3 g((unsigned)ceil_div(a.n, 4), (unsigned)ceil_div(a.d, 256 * BATCH)), b(256);
     if (a.d % 4) LRS_LAUNCH(K_LM_EMBED, (embed_fwd_kernel<WT, OT, true>), g, b, 0, s, a);
     else LRS_LAUNCH(K_LM_EMBED, (embed_fwd_kernel<WT, OT, false>), g, b, 0, s, a);
 }
@@ -228,8 +268,10 @@ void launch_grad(const EmbedArgs& a, hipStream_t s) {
     const int64_t runs = ceil_div(a.n, EMBED_RUN);
     const unsigned of_runs = (unsigned)ceil_div(runs, 4);
     if (a.n > 0) LRS_LAUNCH(K_LM_EMBED_SORT, embed_sort_kernel, dim3((unsigned)ceil_div(a.v, EMBED_ROWS)), dim3(64 * WAVES), 0, s, a);
-    LRS_LAUNCH(K_LM_EMBED_GRAD, (embed_grad_kernel<OT, GT, TAIL>), dim3(of_runs + (unsigned)ceil_div(a.v, 4)), dim3(256), 0, s, a, of_runs);
-    if (a.n > EMBED_RUN) LRS_LAUNCH(K_LM_EMBED_JOIN, (embed_join_kernel<GT, TAIL>), dim3((unsigned)runs), dim3(64 * WAVES), 0, s, a);
+    const unsigned of_rows = (unsigned)std::min<int64_t>(ceil_div(a.v, 4), 2048);
+    LRS_LAUNCH(K_LM_EMBED_GRAD, (embed_grad_kernel<OT, GT, TAIL>), dim3(of_runs + of_rows), dim3(256), 0, s, a, of_runs, (int)of_rows * 4);
+    if (a.n > EMBED_RUN) LRS_LAUNCH(K_LM_EMBED_JOIN, (embed_join_kernel<GT, TAIL>), dim3((unsigned)runs, (unsigned)ceil_div(a.d, 256)),
+                                    dim3(64 * JOIN_WAVES), 0, s, a);
 }
 template <class OT, class GT>
 void launch_grad_tail(const EmbedArgs& a, hipStream_t s) {

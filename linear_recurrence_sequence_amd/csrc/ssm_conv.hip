@@ -9,23 +9,56 @@
 // walks the same way: the g of a token is added to the dx of the W tokens that it came from, which are stored one after
 // the other as they are complete.  A sequence's start clears what is held.
 #include "lm.hpp"
-#include "ssm.hpp"
+#include "ssm_lay.hpp"
 
 namespace lrs {
 namespace {
 
-constexpr int AHEAD = 8;  // tokens whose loads are in flight together
+// Tokens of a block, whose loads are in flight together while the block before is worked on: waves start together, and would else all
+// wait, then all compute.
+constexpr int AHEAD = 4;
+
+// V consecutive channels of a row, at a lane's first channel `col` below d; TAIL: d is no multiple of V.
+template <class T, int V, bool TAIL>
+struct Cols;
+template <class T, bool TAIL>
+struct Cols<T, 4, TAIL> {
+    Quad<T> q;
+    static __device__ __forceinline__ Cols load(const T* row, int col, int d) { return {row_load<T, TAIL>(row, col, d)}; }
+    static __device__ __forceinline__ Cols zero() { return {Quad<T>::zero()}; }
+    __device__ __forceinline__ void get(int col, int d, float* f) const { take<TAIL>(q, col, d, f); }
+    static __device__ __forceinline__ void store(T* row, int col, int d, const float* f) { row_store<T, TAIL>(row, col, d, f); }
+};
+template <class T, bool TAIL>
+struct Cols<T, 2, TAIL> {
+    Pair<T> q;
+    // the channel that a row ends in is loaded as the second of a pair
+    static __device__ __forceinline__ Cols load(const T* row, int col, int d) {
+        if (TAIL && d == 1) return {Pair<T>::one(row)};
+        return {Pair<T>::load(reinterpret_cast<const char*>(row + (TAIL ? min(col, d - 2) : col)), 0)};
+    }
+    static __device__ __forceinline__ Cols zero() { return {Pair<T>{}}; }
+    __device__ __forceinline__ void get(int col, int d, float* f) const {
+        const float2 v = q.get();
+        const bool last = TAIL && col == d - 1;
+        f[0] = last ? v.y : v.x, f[1] = last ? 0.0f : v.y;
+    }
+    static __device__ __forceinline__ void store(T* row, int col, int d, const float* f) {
+        store_pair<T>(reinterpret_cast<char*>(row + col), 0, make_float2(f[0], f[1]), true, !TAIL || col + 1 < d);
+    }
+};
 
 // Which channels and tokens a thread has.
 struct Walk {
     int col, b, piece, t0, t1, len;
     bool on;
 };
+template <int V>
 __device__ __forceinline__ Walk walk_of(const ConvArgs& a) {
-    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x, quads = (a.d + 3) / 4, unit = x / quads;
+    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x, lanes = (a.d + V - 1) / V, unit = x / lanes;
     Walk k;
     k.on = unit < (int64_t)a.batch * a.pieces;
-    k.col = 4 * (int)(x % quads);
+    k.col = V * (int)(x % lanes);
     k.b = (int)(unit / a.pieces);
     k.piece = (int)(unit % a.pieces);
     k.t0 = k.piece * a.tokens;
@@ -34,14 +67,14 @@ __device__ __forceinline__ Walk walk_of(const ConvArgs& a) {
     return k;
 }
 
-template <class T, int W, bool TAIL>
+template <class T, int W, int V, bool TAIL>
 struct Conv {
-    float w[W][4], bias[4];
-    float x[W][4];                              // x[0] the newest input
+    float w[W][V], bias[V];
+    float x[W][V];                              // x[0] the newest input
 
     __device__ __forceinline__ void load(const ConvArgs& a, int col) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < V; ++i) {
             const int c = min(col + i, a.d - 1);
             bias[i] = a.bias ? a.bias[c] : 0.0f;
 #pragma unroll
@@ -50,40 +83,41 @@ struct Conv {
 #pragma unroll
         for (int k = 0; k < W; ++k)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[k][i] = 0.0f;
+            for (int i = 0; i < V; ++i) x[k][i] = 0.0f;
     }
     // A token's input as the next one; a sequence's start forgets the others.
+    template <bool STARTS = true>
     __device__ __forceinline__ void push(const float* v, bool start) {
 #pragma unroll
         for (int k = W - 1; k > 0; --k)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[k][i] = start ? 0.0f : x[k - 1][i];
+            for (int i = 0; i < V; ++i) x[k][i] = STARTS && start ? 0.0f : x[k - 1][i];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[0][i] = v[i];
+        for (int i = 0; i < V; ++i) x[0][i] = v[i];
     }
     // The inputs of the W - 1 tokens before t (padding counts as zero).
     __device__ __forceinline__ void before(const ConvArgs& a, int b, int col, int t, int len) {
-        Quad<T> q[W - 1];
+        Cols<T, V, TAIL> q[W - 1];
         bool start[W - 1];
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
             const int s = t - (W - 1) + k;
             const int64_t row = (int64_t)b * a.length + s;
             start[k] = s >= 0 && a.reset && a.reset[row] != 0;
-            if (s >= 0 && s < len) q[k] = row_load<T, TAIL>(static_cast<const T*>(a.x) + row * a.x_stride, col, a.d);
-            else if (s < 0 && a.state) q[k] = row_load<T, TAIL>(static_cast<const T*>(a.state) + ((int64_t)b * (W - 1) + s + W - 1) * a.d, col, a.d);
-            else q[k] = Quad<T>::zero();
+            if (s >= 0 && s < len) q[k] = Cols<T, V, TAIL>::load(static_cast<const T*>(a.x) + row * a.x_stride, col, a.d);
+            else if (s < 0 && a.state) q[k] = Cols<T, V, TAIL>::load(static_cast<const T*>(a.state) + ((int64_t)b * (W - 1) + s + W - 1) * a.d, col, a.d);
+            else q[k] = Cols<T, V, TAIL>::zero();
         }
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
-            float v[4];
-            take<TAIL>(q[k], col, a.d, v);
+            float v[V];
+            q[k].get(col, a.d, v);
             push(v, start[k]);
         }
     }
     __device__ __forceinline__ void sum(float* p) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < V; ++i) {
             p[i] = bias[i];
 #pragma unroll
             for (int k = W - 1; k >= 0; --k) p[i] = fmaf(w[W - 1 - k][i], x[k][i], p[i]);
@@ -91,127 +125,160 @@ struct Conv {
     }
 };
 
-template <class T, int W, bool TAIL>
+template <class T, int W, int V, bool TAIL>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(const ConvArgs a) {
-    const Walk k = walk_of(a);
+    const Walk k = walk_of<V>(a);
     if (!k.on) return;
-    Conv<T, W, TAIL> c;
+    Conv<T, W, V, TAIL> c;
     c.load(a, k.col);
     if (k.piece == 0 && a.state_out) {          // the inputs before the row's end
         c.before(a, k.b, k.col, k.len, k.len);
         T* to = static_cast<T*>(a.state_out) + (int64_t)k.b * (W - 1) * a.d;
 #pragma unroll
-        for (int i = 0; i < W - 1; ++i) row_store<T, TAIL>(to + (int64_t)(W - 2 - i) * a.d, k.col, a.d, c.x[i]);
+        for (int i = 0; i < W - 1; ++i) Cols<T, V, TAIL>::store(to + (int64_t)(W - 2 - i) * a.d, k.col, a.d, c.x[i]);
     }
     if (k.t0 >= a.length) return;
     c.before(a, k.b, k.col, k.t0, k.len);
     const int64_t row0 = (int64_t)k.b * a.length;
-    for (int t0 = k.t0; t0 < k.t1; t0 += AHEAD) {
-        Quad<T> q[AHEAD];
-        bool start[AHEAD];
+    Cols<T, V, TAIL> next[AHEAD];
+    uint8_t flags[AHEAD] = {};                   // as loaded: joined here, they would be waited for before the block is due
+    const auto fetch = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int64_t row = row0 + min(t0 + i, a.length - 1);
-            q[i] = row_load<T, TAIL>(static_cast<const T*>(a.x) + row * a.x_stride, k.col, a.d);
-            start[i] = a.reset && a.reset[row] != 0;
+            next[i] = Cols<T, V, TAIL>::load(static_cast<const T*>(a.x) + row * a.x_stride, k.col, a.d);
+            if (a.reset) flags[i] = a.reset[row];
         }
+    };
+    fetch(k.t0);
+    for (int t0 = k.t0; t0 < k.t1; t0 += AHEAD) {
+        Cols<T, V, TAIL> q[AHEAD];
+        uint32_t start = 0;                      // bit i: the block's token i starts a sequence
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int t = t0 + i;
-            float v[4], y[4];
-            take<TAIL>(q[i], k.col, a.d, v);
-            c.push(v, start[i]);
-            c.sum(y);
+        for (int i = 0; i < AHEAD; ++i) q[i] = next[i], start |= (flags[i] != 0) << i;
+        if (t0 + AHEAD < k.t1) fetch(t0 + AHEAD);
+        const bool any = t0 + AHEAD > min(k.t1, k.len) || start;
+        both_ways(__any(any), [&](auto some) {  // some: of the wave's tokens start a sequence, or are padding, or behind its piece
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (a.act) y[e] *= sigmoid_of(y[e]);
-                y[e] = t < k.len ? y[e] : 0.0f;  // padding: whatever x holds
+            for (int i = 0; i < AHEAD; ++i) {
+                const int t = t0 + i;
+                float v[V], y[V];
+                q[i].get(k.col, a.d, v);
+                c.template push<decltype(some)::value>(v, start >> i & 1);
+                c.sum(y);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    if (a.act) y[e] *= sigmoid_of(y[e]);
+                    if (decltype(some)::value) y[e] = t < k.len ? y[e] : 0.0f;  // padding: whatever x holds
+                }
+                if (!decltype(some)::value || t < k.t1) Cols<T, V, TAIL>::store(static_cast<T*>(a.y) + (row0 + t) * a.d, k.col, a.d, y);
             }
-            if (t < k.t1) row_store<T, TAIL>(static_cast<T*>(a.y) + (row0 + t) * a.d, k.col, a.d, y);
-        }
+        });
     }
 }
 
-template <class T, int W, bool TAIL>
-__global__ __launch_bounds__(256) void conv_bwd_kernel(const ConvArgs a) {
-    const Walk k = walk_of(a);
+template <class T, int W, int V, bool TAIL>
+__global__ __launch_bounds__(256, V == 2 ? 4 : 1) void conv_bwd_kernel(const ConvArgs a) {
+    const Walk k = walk_of<V>(a);
     if (!k.on) return;
-    Conv<T, W, TAIL> c;
+    Conv<T, W, V, TAIL> c;
     c.load(a, k.col);
     c.before(a, k.b, k.col, k.t0, k.len);
-    float dw[W][4], db[4], dx[W][4];            // dx[j]: of the token j before the newest
+    float dw[W][V], db[V], dx[W][V];            // dx[j]: of the token j before the newest
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < V; ++i) {
         db[i] = 0.0f;
 #pragma unroll
         for (int j = 0; j < W; ++j) dw[j][i] = dx[j][i] = 0.0f;
     }
     const int64_t row0 = (int64_t)k.b * a.length;
-    const int end = k.t1 + W - 1;
     int since = W;                               // tokens since a sequence's start
-    for (int t0 = k.t0; t0 < end; t0 += AHEAD) {
-        Quad<T> q[AHEAD], r[AHEAD];
-        bool start[AHEAD];
+    Cols<T, V, TAIL> next[2][AHEAD];             // x, dy
+    uint8_t flags[AHEAD] = {};
+    const auto fetch = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
             const int64_t row = row0 + max(min(t0 + i, a.length - 1), 0);
             if (a.length > 0) {
-                q[i] = row_load<T, TAIL>(static_cast<const T*>(a.x) + row * a.x_stride, k.col, a.d);
-                r[i] = row_load<T, TAIL>(static_cast<const T*>(a.dy) + row * a.dy_stride, k.col, a.d);
+                next[0][i] = Cols<T, V, TAIL>::load(static_cast<const T*>(a.x) + row * a.x_stride, k.col, a.d);
+                next[1][i] = Cols<T, V, TAIL>::load(static_cast<const T*>(a.dy) + row * a.dy_stride, k.col, a.d);
+                if (a.reset) flags[i] = a.reset[row];
             } else {
-                q[i] = r[i] = Quad<T>::zero();
+                next[0][i] = next[1][i] = Cols<T, V, TAIL>::zero();
             }
-            start[i] = a.reset && t0 + i < k.len && a.reset[row] != 0;
         }
+    };
+    fetch(k.t0);
+    // the W - 1 tokens behind the piece are formed for the dx of its last ones
+    for (int t0 = k.t0; t0 < k.t1 + W - 1; t0 += AHEAD) {
+        Cols<T, V, TAIL> q[AHEAD], r[AHEAD];
+        uint32_t start = 0;
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int t = t0 + i;
-            float v[4], g[4], p[4];
-            take<TAIL>(q[i], k.col, a.d, v);
-            take<TAIL>(r[i], k.col, a.d, g);
-            const bool in = t < k.len;
+        for (int i = 0; i < AHEAD; ++i) q[i] = next[0][i], r[i] = next[1][i], start |= (flags[i] != 0 && t0 + i < k.len) << i;
+        if (t0 + AHEAD < k.t1 + W - 1) fetch(t0 + AHEAD);
+        // a token that needs more than the plain sums: a start, padding, what is behind the piece, or whose dx has a part from the state
+        const bool any = t0 + AHEAD > min(k.t1, k.len) || t0 - (W - 1) < k.t0 || (a.dstate_out && t0 + AHEAD > k.len - (W - 1)) || since < W || start;
+        both_ways(__any(any), [&](auto more) {
+            constexpr bool MORE = decltype(more)::value;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = in ? v[e] : 0.0f;
-            c.push(v, start[i]);
-            c.sum(p);
-            since = start[i] ? 0 : min(since + 1, W);
+            for (int i = 0; i < AHEAD; ++i) {
+                const int t = t0 + i;
+                float v[V], g[V], p[V];
+                q[i].get(k.col, a.d, v);
+                r[i].get(k.col, a.d, g);
+                const bool in = t < k.len;
+                if (MORE) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (a.act) {
-                    const float s = sigmoid_of(p[e]);
-                    g[e] *= s * (1.0f + p[e] * (1.0f - s));
+                    for (int e = 0; e < V; ++e) v[e] = in ? v[e] : 0.0f;
+                    since = start >> i & 1 ? 0 : min(since + 1, W);
                 }
-                g[e] = in ? g[e] : 0.0f;
-                const float mine = t < k.t1 ? g[e] : 0.0f;  // of the tokens behind, dx alone is this piece's
-                db[e] += mine;
+                c.template push<MORE>(v, start >> i & 1);
+                c.sum(p);
 #pragma unroll
-                for (int j = 0; j < W; ++j) dw[W - 1 - j][e] = fmaf(mine, c.x[j][e], dw[W - 1 - j][e]);
+                for (int e = 0; e < V; ++e) {
+                    if (a.act) {
+                        const float s = sigmoid_of(p[e]);
+                        g[e] *= s * fmaf(p[e], 1.0f - s, 1.0f);
+                    }
+                    if (MORE) g[e] = in ? g[e] : 0.0f;
+                    const float mine = !MORE || t < k.t1 ? g[e] : 0.0f;  // of the tokens behind, dx alone is this piece's
+                    db[e] += mine;
 #pragma unroll
-                for (int j = W - 1; j >= 0; --j)
-                    dx[j][e] = fmaf(c.w[W - 1 - j][e], since >= j ? g[e] : 0.0f, j ? dx[j - 1][e] : 0.0f);
-            }
-            // the token that no later one reaches
-            const int done = t - (W - 1), late = done - (k.len - (W - 1));
-            if (late >= 0 && late < W - 1 && a.dstate_out && done < a.length) {
-                bool kept = true;                // its input is in the state that the row leaves
-                for (int s = max(done + 1, 0); s < k.len; ++s) kept = kept && !(a.reset && a.reset[row0 + s] != 0);
-                if (kept) {
-                    float o[4];
-                    take<TAIL>(row_load<T, TAIL>(static_cast<const T*>(a.dstate_out) + ((int64_t)k.b * (W - 1) + late) * a.d, k.col, a.d), k.col,
-                               a.d, o);
+                    for (int j = 0; j < W; ++j) dw[W - 1 - j][e] = fmaf(mine, c.x[j][e], dw[W - 1 - j][e]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) dx[W - 1][e] += o[e];
+                    for (int j = W - 1; j >= 0; --j)
+                        dx[j][e] = fmaf(c.w[W - 1 - j][e], !MORE || since >= j ? g[e] : 0.0f, j ? dx[j - 1][e] : 0.0f);
+                    // here and now: put off to the block's end, these sums would keep all of its inputs in registers
+                    asm volatile("" : "+v"(db[e]));
+#pragma unroll
+                    for (int j = 0; j < W; ++j) asm volatile("" : "+v"(dw[j][e]));
                 }
+                const int done = t - (W - 1);    // the token that no later one reaches
+                if (MORE) {
+                    const int late = done - (k.len - (W - 1));
+                    if (late >= 0 && late < W - 1 && a.dstate_out && done < a.length) {
+                        bool kept = true;        // its input is in the state that the row leaves
+                        for (int s = max(done + 1, 0); s < k.len; ++s) kept = kept && !(a.reset && a.reset[row0 + s] != 0);
+                        if (kept) {
+                            float o[V];
+                            const T* from = static_cast<const T*>(a.dstate_out) + ((int64_t)k.b * (W - 1) + late) * a.d;
+                            Cols<T, V, TAIL>::load(from, k.col, a.d).get(k.col, a.d, o);
+#pragma unroll
+                            for (int e = 0; e < V; ++e) dx[W - 1][e] += o[e];
+                        }
+                    }
+                }
+                if (!MORE || (done >= k.t0 && done < k.t1))
+                    Cols<T, V, TAIL>::store(static_cast<T*>(a.dx) + (row0 + done) * a.d, k.col, a.d, dx[W - 1]);
+                else if (done < 0 && k.piece == 0 && a.dstate)
+                    Cols<T, V, TAIL>::store(static_cast<T*>(a.dstate) + ((int64_t)k.b * (W - 1) + done + W - 1) * a.d, k.col, a.d, dx[W - 1]);
             }
-            if (done >= k.t0 && done < k.t1) row_store<T, TAIL>(static_cast<T*>(a.dx) + (row0 + done) * a.d, k.col, a.d, dx[W - 1]);
-            else if (done < 0 && k.piece == 0 && a.dstate)
-                row_store<T, TAIL>(static_cast<T*>(a.dstate) + ((int64_t)k.b * (W - 1) + done + W - 1) * a.d, k.col, a.d, dx[W - 1]);
-        }
+        });
     }
     float* part = a.part + ((int64_t)k.b * a.pieces + k.piece) * (W + 1) * a.d;
 #pragma unroll
-    for (int j = 0; j < W; ++j) row_store<float, TAIL>(part + (int64_t)j * a.d, k.col, a.d, dw[j]);
-    row_store<float, TAIL>(part + (int64_t)W * a.d, k.col, a.d, db);
+    for (int j = 0; j < W; ++j) Cols<float, V, TAIL>::store(part + (int64_t)j * a.d, k.col, a.d, dw[j]);
+    Cols<float, V, TAIL>::store(part + (int64_t)W * a.d, k.col, a.d, db);
 }
 
 // dw and dbias over the pieces, FP64 in a fixed order: 16 channels a workgroup, 64 lanes down each.  blockIdx.y: a tap, or the bias.
@@ -242,46 +309,50 @@ __global__ __launch_bounds__(1024) void conv_join_kernel(const float* part, int6
 
 // One token: a thread has four channels of a sequence.  (Where d is no multiple of 4 the last thread of a row also loads elements that
 // its neighbour may have moved on already; it uses none of them.)
-template <class T, int W, bool TAIL>
+template <class T, int W, int V, bool TAIL>
 __global__ __launch_bounds__(256) void conv_step_kernel(const ConvArgs a) {
-    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x, quads = (a.d + 3) / 4, b = x / quads;
-    const int col = 4 * (int)(x % quads);
+    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x, lanes = (a.d + V - 1) / V, b = x / lanes;
+    const int col = V * (int)(x % lanes);
     if (b >= a.batch) return;
-    Conv<T, W, TAIL> c;
-    Quad<T> q[W];
+    Conv<T, W, V, TAIL> c;
+    Cols<T, V, TAIL> q[W];
     T* st = static_cast<T*>(const_cast<void*>(a.state)) + b * (W - 1) * a.d;
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) q[k] = row_load<T, TAIL>(st + (int64_t)k * a.d, col, a.d);
-    q[W - 1] = row_load<T, TAIL>(static_cast<const T*>(a.x) + b * a.x_stride, col, a.d);
+    for (int k = 0; k < W - 1; ++k) q[k] = Cols<T, V, TAIL>::load(st + (int64_t)k * a.d, col, a.d);
+    q[W - 1] = Cols<T, V, TAIL>::load(static_cast<const T*>(a.x) + b * a.x_stride, col, a.d);
     c.load(a, col);
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-        float v[4];
-        take<TAIL>(q[k], col, a.d, v);
+        float v[V];
+        q[k].get(col, a.d, v);
         c.push(v, false);
     }
-    float y[4];
+    float y[V];
     c.sum(y);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < V; ++e)
         if (a.act) y[e] *= sigmoid_of(y[e]);
-    row_store<T, TAIL>(static_cast<T*>(a.y) + b * a.d, col, a.d, y);
+    Cols<T, V, TAIL>::store(static_cast<T*>(a.y) + b * a.d, col, a.d, y);
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) row_store<T, TAIL>(st + (int64_t)k * a.d, col, a.d, c.x[W - 2 - k]);
+    for (int k = 0; k < W - 1; ++k) Cols<T, V, TAIL>::store(st + (int64_t)k * a.d, col, a.d, c.x[W - 2 - k]);
 }
 
 enum Kind { FWD, BWD, STEP };
+// Channels of a lane.
+constexpr int FWD_V = 4, BWD_V = 2, STEP_V = 4;
 template <Kind K, class T, int W, bool TAIL>
 void launch_one(const ConvArgs& a, hipStream_t s) {
-    const int64_t threads = ceil_div(a.d, 4) * a.batch * (K == STEP ? 1 : a.pieces);
+    constexpr int V = K == FWD ? FWD_V : K == BWD ? BWD_V : STEP_V;
+    const int64_t threads = ceil_div(a.d, V) * a.batch * (K == STEP ? 1 : a.pieces);
     const dim3 g((unsigned)ceil_div(threads, 256)), b(256);
-    if (K == FWD) LRS_LAUNCH(K_CONV, (conv_fwd_kernel<T, W, TAIL>), g, b, 0, s, a);
-    else if (K == BWD) LRS_LAUNCH(K_CONV_BWD, (conv_bwd_kernel<T, W, TAIL>), g, b, 0, s, a);
-    else LRS_LAUNCH(K_CONV_STEP, (conv_step_kernel<T, W, TAIL>), g, b, 0, s, a);
+    if constexpr (K == FWD) LRS_LAUNCH(K_CONV, (conv_fwd_kernel<T, W, V, TAIL>), g, b, 0, s, a);
+    else if constexpr (K == BWD) LRS_LAUNCH(K_CONV_BWD, (conv_bwd_kernel<T, W, V, TAIL>), g, b, 0, s, a);
+    else LRS_LAUNCH(K_CONV_STEP, (conv_step_kernel<T, W, V, TAIL>), g, b, 0, s, a);
 }
 template <Kind K, class T, int W>
 void launch_tail(const ConvArgs& a, hipStream_t s) {
-    if (a.d % 4) launch_one<K, T, W, true>(a, s);
+    constexpr int V = K == FWD ? FWD_V : K == BWD ? BWD_V : STEP_V;
+    if (a.d % V) launch_one<K, T, W, true>(a, s);
     else launch_one<K, T, W, false>(a, s);
 }
 template <Kind K, class T>
