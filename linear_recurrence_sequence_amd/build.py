@@ -56,12 +56,12 @@ def _compile(src, verbose):
 
 
 def _bind(verbose):
-    """The Python module of the language-model operators' usual calls (host code)."""
+    """The Python module of the operators' usual calls (host code)."""
     import sysconfig
 
     import torch
     at = os.path.dirname(torch.__file__)
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", os.path.join(CSRC, "lm_bind.cpp"), "-o", BIND + ".tmp",
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", *[os.path.join(CSRC, f) for f in ("lm_bind.cpp", "ssm_bind.cpp")], "-o", BIND + ".tmp",
            f"-I{INCLUDE}", f"-I{at}/include", "-I" + sysconfig.get_paths()["include"],
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            f"-L{HERE}", "-l:" + os.path.basename(LIB), f"-L{at}/lib", "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
@@ -70,7 +70,7 @@ def _bind(verbose):
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on lm_bind.cpp:\n{r.stderr}")
+        raise RuntimeError(f"g++ failed on the binding module:\n{r.stderr}")
     os.replace(BIND + ".tmp", BIND)
 
 

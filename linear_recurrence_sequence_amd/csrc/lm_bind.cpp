@@ -7,124 +7,15 @@
 // where a call is not plainly right (lm.py then makes its own checks, says what is
 // wrong, or handles the rarer layout), the library's status where the library
 // refused it, and otherwise the call's results.
-#include <Python.h>
-
-#include <ATen/core/Tensor.h>
-#include <ATen/core/LegacyTypeDispatch.h>
-#include <ATen/ops/as_strided.h>
-#include <ATen/ops/empty.h>
-#include <c10/core/ScalarType.h>
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
+#include "lm_bind.hpp"
 
 #include <vector>
 
 #include "lm_ops.h"
 
+using namespace lrs_bind;
+
 namespace {
-
-using at::Tensor;
-
-// Thrown where the call is left to lm.py.
-struct Leave {};
-
-void need(bool ok) {
-    if (!ok) throw Leave{};
-}
-
-const Tensor& tensor(PyObject* o) {
-    need(THPVariable_Check(o));
-    return THPVariable_Unpack(o);
-}
-
-int code(at::ScalarType t) {
-    need(t == at::kBFloat16 || t == at::kFloat);
-    return t == at::kFloat ? SCAN_F32 : SCAN_BF16;
-}
-
-// Address of a dense device tensor of a type on `dev`.
-void* dense(const Tensor& t, at::ScalarType type, const c10::Device& dev) {
-    need(t.scalar_type() == type && t.device() == dev && t.is_contiguous());
-    return t.data_ptr();
-}
-
-// Elements from one row of t [..., d] to the next: rows of dense columns at one distance.
-int64_t row_stride(const Tensor& t) {
-    const int64_t d = t.size(-1);
-    if (t.is_contiguous()) return d;
-    need(t.stride(-1) == 1 || d == 1);
-    int64_t step = -1, reach = 0;
-    for (int64_t i = t.dim() - 2; i >= 0; --i) {
-        if (t.size(i) == 1) continue;
-        if (step < 0) step = t.stride(i);
-        else need(t.stride(i) == reach);
-        reach = t.stride(i) * t.size(i);
-    }
-    return step < 0 ? d : step;
-}
-
-struct Matrix {
-    void* p = nullptr;
-    int64_t stride = 0;
-};
-Matrix matrix(PyObject* o, const Tensor& like, at::ScalarType type) {
-    if (o == Py_None) return {};
-    const Tensor& t = tensor(o);
-    need(t.scalar_type() == type && t.device() == like.device() && t.sizes() == like.sizes());
-    return {t.data_ptr(), row_stride(t)};
-}
-
-float* vec(PyObject* o, int64_t d, const c10::Device& dev) {
-    if (o == Py_None) return nullptr;
-    const Tensor& t = tensor(o);
-    need(t.dim() == 1 && t.size(0) == d);
-    return static_cast<float*>(dense(t, at::kFloat, dev));
-}
-
-Tensor empty(at::IntArrayRef shape, at::ScalarType type, const c10::Device& dev) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
-}
-
-// The stream given, or the current one; tensors of another device than the current one are left to lm.py.
-PyObject *current_device, *current_stream;  // torch's own, set by setup
-void* stream_of(PyObject* o, const c10::Device& dev) {
-    PyObject* device = PyObject_CallNoArgs(current_device);
-    need(device != nullptr);
-    bool here = PyLong_AsLong(device) == dev.index();
-    if (here && o != Py_None) {  // a stream of the same device
-        PyObject* index = PyObject_GetAttrString(o, "device_index");
-        here = index && PyLong_AsLong(index) == dev.index();
-        Py_XDECREF(index);
-    }
-    PyObject* raw = !here ? nullptr : o == Py_None ? PyObject_CallOneArg(current_stream, device) : PyObject_GetAttrString(o, "cuda_stream");
-    Py_DECREF(device);
-    need(raw != nullptr);
-    void* s = PyLong_AsVoidPtr(raw);
-    Py_DECREF(raw);
-    need(!PyErr_Occurred());
-    return s;
-}
-double number(PyObject* o) {
-    const double v = PyFloat_AsDouble(o);
-    need(!PyErr_Occurred());
-    return v;
-}
-
-// Runs f, which returns a new reference; no C++ exception crosses into Python.
-template <class F>
-PyObject* guarded(F f) {
-    HANDLE_TH_ERRORS
-    at::AutoDispatchBelowADInplaceOrView below;  // what is made here has no gradient of its own
-    try {
-        return f();
-    } catch (const Leave&) {
-        PyErr_Clear();
-        Py_RETURN_NONE;
-    }
-    END_HANDLE_TH_ERRORS
-}
-
-PyObject* status(scan_status st) { return PyLong_FromLong(st); }
 
 struct Norm {
     const Tensor& x;
@@ -166,12 +57,6 @@ PyObject* block_norm_fwd(PyObject*, PyObject* const* a, Py_ssize_t count) {
         if (s != SCAN_OK) return status(s);
         return Py_BuildValue("(NNN)", THPVariable_Wrap(r), THPVariable_Wrap(n), THPVariable_Wrap(stats));
     });
-}
-
-void put(PyObject* dict, const char* key, const Tensor& t) {
-    PyObject* o = THPVariable_Wrap(t);
-    PyDict_SetItemString(dict, key, o);
-    Py_DECREF(o);
 }
 
 // (x, y, gate, w_post, scale, w_pre, stats, dr, dn, act, stream) -> dict
@@ -297,7 +182,7 @@ struct List {
     // says to autograd that a call wrote the tensors (5 ns each: of a step's, the weights, which graphs keep)
     void written() const {
         for (Py_ssize_t i = 0; fast && i < size(); ++i)
-            if (!(*this)[i].is_inference()) (*this)[i].unsafeGetTensorImpl()->bump_version();
+            lrs_bind::written((*this)[i]);
     }
     template <class T>
     T* const* as() {
@@ -351,6 +236,50 @@ PyObject* adamw_step(PyObject*, PyObject* const* a, Py_ssize_t count) {
     });
 }
 
+// (tokens, w, scale, out in FP32: True, False or None (as w), stream) -> out
+PyObject* embed_fwd(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    return guarded([&]() -> PyObject* {
+        need(count == 5);
+        const Tensor &t = tensor(a[0]), &w = tensor(a[1]);
+        const c10::Device dev = w.device();
+        need(dev.is_cuda() && w.dim() == 2 && w.size(0) >= 1 && w.size(1) >= 1);
+        const int wt = code(w.scalar_type());
+        const int64_t* pt = static_cast<const int64_t*>(dense(t, at::kLong, dev));
+        const void* pw = dense(w, w.scalar_type(), dev);
+        const at::ScalarType type = a[3] == Py_None ? w.scalar_type() : a[3] == Py_True ? at::kFloat : at::kBFloat16;
+        std::vector<int64_t> shape(t.sizes().begin(), t.sizes().end());
+        shape.push_back(w.size(1));
+        need(w.size(1) <= (1 << 23));
+        Tensor out = empty(shape, type, dev);
+        const scan_status s = lm_embed_fwd(t.numel(), (int)w.size(1), w.size(0), wt, code(type), number(a[2]), pt, pw, out.data_ptr(), stream_of(a[4], dev));
+        if (s != SCAN_OK) return status(s);
+        return THPVariable_Wrap(out);
+    });
+}
+
+// (tokens, dout, v, scale, gradient in FP32, stream) -> dw
+PyObject* embed_bwd(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    return guarded([&]() -> PyObject* {
+        need(count == 6);
+        const Tensor &t = tensor(a[0]), &g = tensor(a[1]);
+        const c10::Device dev = g.device();
+        need(dev.is_cuda() && g.dim() >= 1 && g.size(-1) >= 1 && g.size(-1) <= (1 << 23) && t.sizes() == g.sizes().slice(0, g.dim() - 1) && PyLong_Check(a[2]));
+        const long long v = PyLong_AsLongLong(a[2]);
+        need(!PyErr_Occurred() && v >= 1);
+        const int64_t d = g.size(-1), n = t.numel(), *pt = static_cast<const int64_t*>(dense(t, at::kLong, dev));
+        const int gt = code(g.scalar_type());
+        const int64_t stride = row_stride(g);
+        const size_t bytes = lm_embed_bwd_workspace_bytes(n, (int)d, v);
+        need(bytes > 0);
+        const at::ScalarType type = a[4] == Py_True ? at::kFloat : at::kBFloat16;
+        Tensor dw = empty({v, d}, type, dev), ws = empty({(int64_t)bytes}, at::kByte, dev);
+        const scan_status s = lm_embed_bwd(n, (int)d, v, gt, code(type), number(a[3]), pt, g.data_ptr(), stride, 0, dw.data_ptr(), ws.data_ptr(), bytes,
+                                           stream_of(a[5], dev));
+        if (s != SCAN_OK) return status(s);
+        return THPVariable_Wrap(dw);
+    });
+}
+
 // (torch's function for the current device, and for the current stream's address of a device)
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t count) {
     if (count != 2) {
@@ -366,7 +295,9 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t count) {
 
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD(block_norm_fwd), METHOD(block_norm_bwd), METHOD(linear_ce_fwd), METHOD(linear_ce_bwd),
-                         METHOD(adamw_step),     METHOD(setup),          {nullptr, nullptr, 0, nullptr}};
+                         METHOD(adamw_step),     METHOD(embed_fwd),      METHOD(embed_bwd),     METHOD(ssm_scan_fwd),
+                         METHOD(ssm_scan_bwd),   METHOD(ssm_scan_step),  METHOD(causal_conv_fwd), METHOD(causal_conv_bwd),
+                         METHOD(causal_conv_step), METHOD(setup),          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_lm_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -94,6 +94,9 @@ struct Pair<uint16_t> {
     uint32_t w;
     static __device__ __forceinline__ Pair load(const char* base, uint32_t off) { return {*reinterpret_cast<const u32_a2*>(base + off)}; }
     static __device__ __forceinline__ Pair one(const uint16_t* p) { return {(uint32_t)*p << 16}; }  // as the second
+    static __device__ __forceinline__ Pair load(const char* base, uint32_t off, bool single) {
+        return single ? one(reinterpret_cast<const uint16_t*>(base + off)) : load(base, off);
+    }
     __device__ __forceinline__ float2 get() const { return make_float2(bf16_lo(w), bf16_hi(w)); }
 };
 template <>
@@ -101,6 +104,9 @@ struct Pair<float> {
     f32x2_t w;
     static __device__ __forceinline__ Pair load(const char* base, uint32_t off) { return {*reinterpret_cast<const f32x2_a4*>(base + off)}; }
     static __device__ __forceinline__ Pair one(const float* p) { return {f32x2_t{0.0f, *p}}; }
+    static __device__ __forceinline__ Pair load(const char* base, uint32_t off, bool single) {
+        return single ? one(reinterpret_cast<const float*>(base + off)) : load(base, off);
+    }
     __device__ __forceinline__ float2 get() const { return make_float2(w[0], w[1]); }
 };
 

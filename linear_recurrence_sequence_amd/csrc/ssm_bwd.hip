@@ -30,20 +30,23 @@ __device__ __forceinline__ void load_chunk(const SsmArgs& a, const Place& p, int
     const int left = a.length - chunk * SSM_TOK, g = fresh_lane() / Lay<NG>::J;
     const char *u = rows_at<T>(a.u, row0, a.u_stride), *dt = rows_at<T>(a.dt, row0, a.dt_stride), *z = rows_at<T>(a.z, row0, a.z_stride),
             *dy = rows_at<T>(a.dy, row0, a.dy_stride);
+    both_ways(a.d == 1, [&](auto one) {
+        constexpr bool single = decltype(one)::value;
 #pragma unroll
-    for (int q = 0; q < Lay<NG>::Q; ++q) {
-        const int r = min(q * NG + g, left - 1);
-        if (!SUM) v.u[q] = Pair<T>::load(u, row_off<T>(r, a.u_stride, p.i));
-        v.dt[q] = Pair<T>::load(dt, row_off<T>(r, a.dt_stride, p.i));
-        v.dy[q] = Pair<T>::load(dy, row_off<T>(r, a.dy_stride, p.i));
-        if (GATE) v.z[q] = Pair<T>::load(z, row_off<T>(r, a.z_stride, p.i));
-    }
+        for (int q = 0; q < Lay<NG>::Q; ++q) {
+            const int r = min(q * NG + g, left - 1);
+            if (!SUM) v.u[q] = Pair<T>::load(u, row_off<T>(r, a.u_stride, p.i), single);
+            v.dt[q] = Pair<T>::load(dt, row_off<T>(r, a.dt_stride, p.i), single);
+            v.dy[q] = Pair<T>::load(dy, row_off<T>(r, a.dy_stride, p.i), single);
+            if (GATE) v.z[q] = Pair<T>::load(z, row_off<T>(r, a.z_stride, p.i), single);
+        }
+    });
     if (!SUM) load_group<T, NG>(a.b, a.b_stride, row0, left, p.gr, a.n, v.b);
     load_group<T, NG>(a.c, a.c_stride, row0, left, p.gr, a.n, v.c);
     if (!SUM) {
         const char* at = reinterpret_cast<const char*>(a.saved + ((int64_t)p.b * a.plan.chunks + chunk) * a.n * a.d);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) v.h[s] = Pair<float>::load(at, state_off(a, min(4 * g + s, a.n - 1), p.i));
+        for (int s = 0; s < 4; ++s) v.h[s] = Pair<float>::load(at, state_off(a, min(4 * g + s, a.n - 1), p.i), a.d == 1);
     }
 }
 
@@ -68,7 +71,7 @@ __global__ __launch_bounds__(256) void ssm_rev_kernel(const SsmArgs a) {
     float A[2][4], G[2][4] = {};
     bool okn[4];
     load_rates(a, p, A, okn);
-    const float2 bias = load_two(a.dt_bias, p);
+    const float2 bias = load_two(a, a.dt_bias, p);
     float2 total = make_float2(0.f, 0.f);
     bool anew = false;
     const int first = seg * a.plan.seg, last = min(first + a.plan.seg, a.plan.chunks);
@@ -166,7 +169,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const SsmArgs a)
     through_segments(a, p, segs - 1, seg, -1, G);  // what those behind this one hand on
 #pragma unroll
     for (int s = 0; s < 4; ++s) G[0][s] = p.ok0 && okn[s] ? G[0][s] : 0.0f, G[1][s] = p.ok1 && okn[s] ? G[1][s] : 0.0f;
-    const float2 bias = load_two(a.dt_bias, p), skip = load_two(a.skip, p);
+    const float2 bias = load_two(a, a.dt_bias, p), skip = load_two(a, a.skip, p);
     float2 dskip = make_float2(0.f, 0.f), dbias = make_float2(0.f, 0.f);
     const int first = seg * a.plan.seg, last = min(first + a.plan.seg, a.plan.chunks);
     Chunk<T, NG> v;
@@ -385,7 +388,13 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(const SsmArgs a, unsigned
         if (n >= a.n) return;
         const float* at = a.part_bc + ((int64_t)gr * a.plan.blocks * rows + row) * 2 * n4 + k * n4 + n;
         float w = 0.0f;
-        for (int i = 0; i < a.plan.blocks; ++i) w += at[(int64_t)i * rows * 2 * n4];
+        for (int i0 = 0; i0 < a.plan.blocks; i0 += 8) {
+            float v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v[u] = at[(int64_t)min(i0 + u, a.plan.blocks - 1) * rows * 2 * n4];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) w += i0 + u < a.plan.blocks ? v[u] : 0.0f;
+        }
         store_value(static_cast<T*>(k ? a.db : a.dc) + (row * a.groups + gr) * a.n + n, w);
         return;
     }
@@ -396,7 +405,13 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(const SsmArgs a, unsigned
     const float* at = rate ? a.part_a + (int64_t)n * a.d + i : a.part_d + (int64_t)(n - a.n) * a.d + i;
     const int64_t step = rate ? (int64_t)a.n * a.d : 2 * (int64_t)a.d;
     double w = 0.0;
-    for (int k = 0; k < parts; ++k) w += (double)at[k * step];
+    for (int k0 = 0; k0 < parts; k0 += 8) {
+        float v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = at[min(k0 + u, parts - 1) * step];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) w += k0 + u < parts ? (double)v[u] : 0.0;
+    }
     float* out = rate ? a.da + (int64_t)i * a.n + n : n == a.n ? (a.dskip ? a.dskip + i : nullptr) : (a.ddt_bias ? a.ddt_bias + i : nullptr);
     if (out) *out = (float)w;
 }

@@ -27,13 +27,15 @@ __device__ __forceinline__ void load_chunk(const SsmArgs& a, const Place& p, int
     const int64_t row0 = (int64_t)p.b * a.length + chunk * SSM_TOK;
     const int left = a.length - chunk * SSM_TOK, g = fresh_lane() / Lay<NG>::J;
     const char *u = rows_at<T>(a.u, row0, a.u_stride), *dt = rows_at<T>(a.dt, row0, a.dt_stride), *z = rows_at<T>(a.z, row0, a.z_stride);
+    both_ways(a.d == 1, [&](auto single) {
 #pragma unroll
-    for (int q = 0; q < Lay<NG>::Q; ++q) {
-        const int r = min(q * NG + g, left - 1);
-        v.u[q] = Pair<T>::load(u, row_off<T>(r, a.u_stride, p.i));
-        v.dt[q] = Pair<T>::load(dt, row_off<T>(r, a.dt_stride, p.i));
-        if (!SUM && GATE) v.z[q] = Pair<T>::load(z, row_off<T>(r, a.z_stride, p.i));
-    }
+        for (int q = 0; q < Lay<NG>::Q; ++q) {
+            const int r = min(q * NG + g, left - 1);
+            v.u[q] = Pair<T>::load(u, row_off<T>(r, a.u_stride, p.i), decltype(single)::value);
+            v.dt[q] = Pair<T>::load(dt, row_off<T>(r, a.dt_stride, p.i), decltype(single)::value);
+            if (!SUM && GATE) v.z[q] = Pair<T>::load(z, row_off<T>(r, a.z_stride, p.i), decltype(single)::value);
+        }
+    });
     load_group<T, NG>(a.b, a.b_stride, row0, left, p.gr, a.n, v.b);
     if (!SUM) load_group<T, NG>(a.c, a.c_stride, row0, left, p.gr, a.n, v.c);
 }
@@ -72,7 +74,7 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(const SsmArgs a) {
     if (!SUM) through_segments(a, p, 0, seg, 1, h);  // what those before this one leave
 #pragma unroll
     for (int s = 0; s < 4; ++s) h[0][s] = p.ok0 && okn[s] ? h[0][s] : 0.0f, h[1][s] = p.ok1 && okn[s] ? h[1][s] : 0.0f;
-    const float2 bias = load_two(a.dt_bias, p), skip = load_two(SUM ? nullptr : a.skip, p);
+    const float2 bias = load_two(a, a.dt_bias, p), skip = load_two(a, SUM ? nullptr : a.skip, p);
     float2 total = make_float2(0.f, 0.f);
     bool anew = false;
     const int first = seg * a.plan.seg, last = min(first + a.plan.seg, a.plan.chunks);

@@ -44,8 +44,8 @@ __device__ __forceinline__ Place place_of(const SsmArgs& a, int tile, int gr, in
     p.g = lane / Lay<NG>::J, p.j = lane % Lay<NG>::J;
     p.c0 = gr * a.per + tile * Lay<NG>::CH + 2 * p.j;
     p.ok0 = p.c0 < end, p.ok1 = p.c0 + 1 < end;
-    p.i = max(min(p.c0, end - 2), 0);  // d is at least 2
-    p.odd = p.c0 == p.i + 1;
+    p.i = max(min(p.c0, end - 2), 0);
+    p.odd = p.c0 == p.i + 1 || a.d == 1;  // of one channel in all, that one is loaded as the second
     return p;
 }
 
@@ -121,9 +121,10 @@ __device__ __forceinline__ void load_rates(const SsmArgs& a, const Place& p, flo
     }
 }
 // Two of a vector's values.
-__device__ __forceinline__ float2 load_two(const float* v, const Place& p) {
+__device__ __forceinline__ float2 load_two(const SsmArgs& a, const float* v, const Place& p) {
     if (!v) return make_float2(0.f, 0.f);
-    return make_float2(v[p.odd ? p.i + 1 : p.i], v[p.i + 1]);
+    const int last = p.i + (a.d > 1 ? 1 : 0);
+    return make_float2(v[p.odd ? last : p.i], v[last]);
 }
 
 // What a segment from nothing leaves: the product of its decays (0 behind a sequence's start) and its state or cotangent.
@@ -161,8 +162,8 @@ __device__ __forceinline__ void through_segments(const SsmArgs& a, const Place& 
             const char* at = reinterpret_cast<const char*>(a.part + ((int64_t)p.b * a.plan.segments + from + step * min(i0 + u, count - 1)) * one);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                decay[u][s] = Pair<float>::load(at, off[s]);
-                left[u][s] = Pair<float>::load(at + one * 2, off[s]);
+                decay[u][s] = Pair<float>::load(at, off[s], a.d == 1);
+                left[u][s] = Pair<float>::load(at + one * 2, off[s], a.d == 1);
             }
         }
 #pragma unroll

@@ -52,7 +52,7 @@ inline SsmPlan ssm_plan(int64_t batch, int64_t length, int d, int n, int groups,
 
 inline bool ssm_shape(int64_t batch, int64_t length, int d, int n, int groups) {
     return batch >= 0 && length >= 0 && length <= 0x7fffff00 && batch <= 0x7fffffff && (length == 0 || batch <= 0x7fffffff / length) &&
-           d >= 2 && d <= (1 << 21) && groups >= 1 && d % groups == 0 && n >= 1 && n <= SSM_MOST_N;
+           d >= 1 && d <= (1 << 21) && groups >= 1 && d % groups == 0 && n >= 1 && n <= SSM_MOST_N;
 }
 
 // Sizes that the launches cover: workgroups of 256 threads, and element counts within 62 bits.

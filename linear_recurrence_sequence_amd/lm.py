@@ -433,6 +433,12 @@ def embed_fwd(tokens, w, *, scale=1.0, out_dtype=None, out=None, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return embed_fwd(tokens, w, scale=scale, out_dtype=out_dtype, out=out)
+    if out is None and (out_dtype is None or out_dtype in _DTYPES):
+        r = _native().embed_fwd(tokens, w, scale, None if out_dtype is None else out_dtype is _F32, None)
+        if isinstance(r, torch.Tensor):
+            return r
+        if r is not None:
+            _check(r, "lm_embed_fwd")
     _want(tokens, "tokens", torch.int64)
     _want(w, "w", _DTYPES)
     if w.dim() != 2 or w.shape[0] < 1 or w.shape[1] < 1:
@@ -464,6 +470,12 @@ def embed_bwd(tokens, dout, v, *, scale=1.0, grad_dtype=_BF16, dw=None, accumula
     if stream is not None:
         with torch.cuda.stream(stream):
             return embed_bwd(tokens, dout, v, scale=scale, grad_dtype=grad_dtype, dw=dw, accumulate=accumulate, workspace=workspace)
+    if dw is None and workspace is None and not accumulate and grad_dtype in _DTYPES:
+        r = _native().embed_bwd(tokens, dout, v, scale, grad_dtype is _F32, None)
+        if isinstance(r, torch.Tensor):
+            return r
+        if r is not None:
+            _check(r, "lm_embed_bwd")
     _want(tokens, "tokens", torch.int64)
     _want(dout, "dout", _DTYPES)
     if dout.dim() < 1 or dout.shape[:-1] != tokens.shape or dout.shape[-1] < 1:

@@ -8,7 +8,8 @@ one given.  The differentiable forms are in autograd.py.
 
 With a stream given a call runs as if that stream were the current one: its
 outputs and workspace are allocated there.  Tensors lie on the current device,
-or the stream's.
+or the stream's.  The usual calls, right and with outputs of their own, go through
+_lm_bind (csrc/ssm_bind.cpp); every other one is checked, and where it is wrong refused, here.
 
 Rows of activations may lie apart (views of a wider projection).  In all calls
 over several tokens, reset [batch, length] (uint8 or bool) marks tokens that
@@ -21,7 +22,7 @@ import ctypes
 import torch
 
 from . import scan
-from .lm import _dense, _p, _row_stride, _same_device, _written
+from .lm import _dense, _native, _p, _row_stride, _same_device, _written
 from .scan import _check, _code, _nbytes, _stream, _want, _want_bytes
 
 _BF16, _F32 = torch.bfloat16, torch.float32
@@ -137,6 +138,12 @@ def ssm_scan_fwd(u, dt, a, b, c, d=None, z=None, dt_bias=None, h0=None, *, softp
         with torch.cuda.stream(stream):
             return ssm_scan_fwd(u, dt, a, b, c, d, z, dt_bias, h0, softplus=softplus, reset=reset, lengths=lengths, want_saved=want_saved, y=y,
                                 h_final=h_final, workspace=workspace)
+    if y is None and h_final is None and workspace is None:
+        out = _native().ssm_scan_fwd(u, dt, a, b, c, d, z, dt_bias, h0, softplus, reset, lengths, want_saved, None)
+        if out.__class__ is tuple:
+            return out
+        if out is not None:
+            _check(out, "ssm_scan_fwd")
     width, n, groups, su, sdt, sb, sc, sz = _scan_args(u, dt, a, b, c, d, z, dt_bias, 3)
     batch, length, _ = u.shape
     _want(h0, "h0", _F32, (batch, width, n), optional=True)
@@ -169,6 +176,12 @@ def ssm_scan_bwd(u, dt, a, b, c, d, z, dt_bias, saved, dy, dh_final=None, *, sof
         with torch.cuda.stream(stream):
             return ssm_scan_bwd(u, dt, a, b, c, d, z, dt_bias, saved, dy, dh_final, softplus=softplus, reset=reset, lengths=lengths,
                                 want_dh0=want_dh0, workspace=workspace)
+    if workspace is None:
+        out = _native().ssm_scan_bwd(u, dt, a, b, c, d, z, dt_bias, saved, dy, dh_final, softplus, reset, lengths, want_dh0, None)
+        if out.__class__ is dict:
+            return out
+        if out is not None:
+            _check(out, "ssm_scan_bwd")
     width, n, groups, su, sdt, sb, sc, sz = _scan_args(u, dt, a, b, c, d, z, dt_bias, 3)
     batch, length, _ = u.shape
     _sequence_args((batch, length), reset, lengths)
@@ -208,6 +221,12 @@ def ssm_scan_step(h, u, dt, a, b, c, d=None, z=None, dt_bias=None, *, softplus=T
     if stream is not None:
         with torch.cuda.stream(stream):
             return ssm_scan_step(h, u, dt, a, b, c, d, z, dt_bias, softplus=softplus, y=y)
+    if y is None:
+        out = _native().ssm_scan_step(h, u, dt, a, b, c, d, z, dt_bias, softplus, None)
+        if isinstance(out, torch.Tensor):
+            return out
+        if out is not None:
+            _check(out, "ssm_scan_step")
     width, n, groups, su, sdt, sb, sc, sz = _scan_args(u, dt, a, b, c, d, z, dt_bias, 2)
     batch = u.shape[0]
     _want(h, "h", _F32, (batch, width, n))
@@ -256,6 +275,12 @@ def causal_conv_fwd(x, w, bias=None, *, act="silu", state=None, reset=None, leng
     if stream is not None:
         with torch.cuda.stream(stream):
             return causal_conv_fwd(x, w, bias, act=act, state=state, reset=reset, lengths=lengths, y=y, state_out=state_out)
+    if y is None and state_out is None and act in ACTS:
+        out = _native().causal_conv_fwd(x, w, bias, ACTS[act], state, reset, lengths, None)
+        if out.__class__ is tuple:
+            return out
+        if out is not None:
+            _check(out, "ssm_conv_fwd")
     d, width, sx = _conv_args(x, w, bias, act, 3)
     batch, length, _ = x.shape
     _conv_state(state, "state", x, width)
@@ -278,6 +303,12 @@ def causal_conv_bwd(x, w, bias, dy, dstate_out=None, *, act="silu", state=None, 
     if stream is not None:
         with torch.cuda.stream(stream):
             return causal_conv_bwd(x, w, bias, dy, dstate_out, act=act, state=state, reset=reset, lengths=lengths, workspace=workspace)
+    if workspace is None and act in ACTS:
+        out = _native().causal_conv_bwd(x, w, bias, dy, dstate_out, ACTS[act], state, reset, lengths, None)
+        if out.__class__ is dict:
+            return out
+        if out is not None:
+            _check(out, "ssm_conv_bwd")
     d, width, sx = _conv_args(x, w, bias, act, 3)
     batch, length, _ = x.shape
     _conv_state(state, "state", x, width)
@@ -304,6 +335,12 @@ def causal_conv_step(x, w, bias, state, *, act="silu", y=None, stream=None):
     if stream is not None:
         with torch.cuda.stream(stream):
             return causal_conv_step(x, w, bias, state, act=act, y=y)
+    if y is None and act in ACTS:
+        out = _native().causal_conv_step(x, w, bias, state, ACTS[act], None)
+        if isinstance(out, torch.Tensor):
+            return out
+        if out is not None:
+            _check(out, "ssm_conv_step")
     d, width, sx = _conv_args(x, w, bias, act, 2)
     _conv_state(state, "state", x, width, optional=False)
     given = y
