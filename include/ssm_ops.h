@@ -18,6 +18,8 @@
  * there on are padding: their outputs and gradients are zero, what their
  * inputs hold is not used, and the state behind a row is the one after its
  * last token.  A length outside 0..length counts as the nearest of the two.
+ * A flag in the padding starts an empty sequence for the scan, whose state behind
+ * the row is then zero; the convolution looks at no flags there.
  */
 #ifndef SSM_OPS_H
 #define SSM_OPS_H

@@ -81,7 +81,7 @@ __global__ __launch_bounds__(256) void ssm_rev_kernel(const SsmArgs a) {
         const uint32_t lane = fresh_lane();
         const int g = lane / J, j = lane % J;
         const int t0 = chunk * SSM_TOK, live = len - t0;
-        const uint32_t resets = resets_of(a, b, t0, len);
+        const uint32_t resets = resets_of(a, b, t0);
         anew |= resets != 0;
         const auto stage = [&](auto mask, auto soft) {
 #pragma unroll
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const SsmArgs a)
         const int g = lane / J, j = lane % J;
         const int t0 = chunk * SSM_TOK, live = len - t0, left = a.length - t0;
         const int64_t row0 = (int64_t)b * a.length + t0;
-        const uint32_t resets = resets_of(a, b, t0, len);
+        const uint32_t resets = resets_of(a, b, t0);
         float hin[2][4];
         const auto stage = [&](auto mask, auto soft) {
 #pragma unroll

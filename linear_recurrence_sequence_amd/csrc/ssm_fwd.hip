@@ -90,7 +90,7 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(const SsmArgs a) {
             for (int s = 0; s < 4; ++s)
                 if (okn[s]) store_pair<float>(at, state_off(a, 4 * g + s, p.c0), make_float2(h[0][s], h[1][s]), p.ok0, p.ok1);
         }
-        const uint32_t resets = resets_of(a, b, t0, len);
+        const uint32_t resets = resets_of(a, b, t0);
         anew |= resets != 0;
         float2 us[Q], gate[Q];
         const auto stage = [&](auto mask, auto soft) {

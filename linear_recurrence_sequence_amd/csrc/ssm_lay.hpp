@@ -56,11 +56,11 @@ __device__ __forceinline__ int length_of(const SsmArgs& a, int b) {
     return a.lengths ? min(max(a.lengths[b], 0), a.length) : a.length;
 }
 
-// Bit t: token t0 + t of row b starts a sequence.
-__device__ __forceinline__ uint32_t resets_of(const SsmArgs& a, int b, int t0, int len) {
+// Bit t: token t0 + t of row b starts a sequence, in the padding too.
+__device__ __forceinline__ uint32_t resets_of(const SsmArgs& a, int b, int t0) {
     if (!a.reset) return 0u;
     const int t = t0 + (threadIdx.x & 63);
-    const bool r = t < min(t0 + SSM_TOK, len) && a.reset[(int64_t)b * a.length + t] != 0;
+    const bool r = t < min(t0 + SSM_TOK, a.length) && a.reset[(int64_t)b * a.length + t] != 0;
     return (uint32_t)__ballot(r);
 }
 

@@ -53,7 +53,7 @@ def scan_ref(u, dt, a, b, c, d=None, z=None, dt_bias=None, h0=None, *, softplus=
         gate, gate_slope = size(z * sg), sg * (1 + size(z) * (1 - sg)) if absolute else sg * (1 + z * (1 - sg))
     keep = torch.ones((batch, length), dtype=torch.bool, device=dev)
     if reset is not None:
-        keep = ~((reset != 0) & (on != 0))
+        keep = reset == 0                                        # in the padding too
 
     def spread(x):                                              # [batch, groups, n] to [batch, width, n]
         return x.repeat_interleave(per, 1)
