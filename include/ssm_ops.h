@@ -43,8 +43,8 @@ extern "C" {
  *   u, dt, z  [batch, length, d] of dtype;  b, c  [batch, length, groups, n] of
  *   dtype, a row's groups * n values dense;  a f32 [d, n];  skip (d above) and
  *   dt_bias f32 [d], NULL = 0;  h0 f32 [batch, d, n], NULL = 0.
- * batch, length >= 0, d >= 1 and a multiple of groups, 1 <= n <= SSM_MAX_STATE,
- * batch * length < 2^31.
+ * batch, length >= 0, 1 <= d <= 2^21 and a multiple of groups, 1 <= n <= SSM_MAX_STATE,
+ * batch * length < 2^31, row strides below 2^22.
  * ====================================================================== */
 #define SSM_MAX_STATE 64
 /* Tokens between two states that the forward keeps for the backward. */
@@ -99,6 +99,7 @@ scan_status ssm_scan_step(int64_t batch, int d, int n, int groups, int dtype, in
  * sequence of the row count as zero.  Arithmetic is FP32, y is rounded once.
  *   x      [batch, length, d] of dtype;  w f32 [d, width];  bias f32 [d], NULL = 0
  *   state  [batch, width - 1, d] of dtype, dense, the oldest input first
+ * batch, length >= 0, 1 <= d <= 2^24, batch * length < 2^31.
  * ====================================================================== */
 enum { CONV_NONE = 0, CONV_SILU = 1 };
 #define CONV_MAX_WIDTH 4

@@ -14,9 +14,9 @@ namespace {
 
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
 
-scan_status check_strides(const char* fn, std::initializer_list<int64_t> strides) {
+scan_status check_strides(const char* fn, std::initializer_list<int64_t> strides, int64_t most = kMaxStride) {
     for (int64_t s : strides)
-        if (s < 0 || s > kMaxStride) return fail(SCAN_ERR_SHAPE, std::string(fn) + ": row strides must not be negative");
+        if (s < 0 || s > most) return fail(SCAN_ERR_SHAPE, std::string(fn) + ": row strides must lie in 0.." + std::to_string(most));
     return SCAN_OK;
 }
 
@@ -28,7 +28,7 @@ scan_status ssm_check(const char* fn, int64_t batch, int64_t length, int d, int 
                                         " (need d a multiple of groups, 1 <= n <= " + std::to_string(SSM_MAX_STATE) +
                                         ", batch * length < 2^31 and launches below 2^32 threads)");
     if (!dtype_ok(dtype)) return fail(SCAN_ERR_SHAPE, std::string(fn) + ": dtype must be SCAN_BF16 or SCAN_F32");
-    return check_strides(fn, strides);
+    return check_strides(fn, strides, SSM_MOST_STRIDE);
 }
 
 scan_status check_workspace(const char* fn, size_t have, size_t need) {

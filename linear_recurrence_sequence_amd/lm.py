@@ -481,7 +481,7 @@ def embed_bwd(tokens, dout, v, *, scale=1.0, grad_dtype=_BF16, dw=None, accumula
     if dout.dim() < 1 or dout.shape[:-1] != tokens.shape or dout.shape[-1] < 1:
         raise ValueError(f"dout must be [..., d] with the tokens' shape in front, got shapes {tuple(dout.shape)} and {tuple(tokens.shape)}")
     _dense(tokens, "tokens")
-    n, d, v = tokens.numel(), dout.shape[-1], int(v)
+    n, d, v, sg = tokens.numel(), dout.shape[-1], int(v), _row_stride(dout, "dout")
     if accumulate and dw is None:
         raise ValueError("accumulate needs a dw to add to")
     given = dw
@@ -499,7 +499,7 @@ def embed_bwd(tokens, dout, v, *, scale=1.0, grad_dtype=_BF16, dw=None, accumula
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dout.device)
     _want_bytes(workspace, "workspace", need)
-    st = lib().lm_embed_bwd(n, d, v, _code(dout.dtype), _code(dw.dtype), scale, _p(tokens), _p(dout), _row_stride(dout, "dout"), int(bool(accumulate)),
+    st = lib().lm_embed_bwd(n, d, v, _code(dout.dtype), _code(dw.dtype), scale, _p(tokens), _p(dout), sg, int(bool(accumulate)),
                             _p(dw), _p(workspace), _nbytes(workspace), _stream(None))
     _check(st, "lm_embed_bwd")
     _written(given)

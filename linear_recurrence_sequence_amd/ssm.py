@@ -186,6 +186,7 @@ def ssm_scan_bwd(u, dt, a, b, c, d, z, dt_bias, saved, dy, dh_final=None, *, sof
     batch, length, _ = u.shape
     _sequence_args((batch, length), reset, lengths)
     _want(dy, "dy", u.dtype, u.shape)
+    sdy = _row_stride(dy, "dy")
     _want(dh_final, "dh_final", _F32, (batch, width, n), optional=True)
     _dense(dh_final, "dh_final")
     dev = u.device
@@ -207,7 +208,7 @@ def ssm_scan_bwd(u, dt, a, b, c, d, z, dt_bias, saved, dy, dh_final=None, *, sof
         out["dh0"] = torch.empty((batch, width, n), **group)
     o = {k: _p(t) for k, t in out.items()}
     st = lib().ssm_scan_bwd(batch, length, width, n, groups, _code(u.dtype), int(bool(softplus)), _p(u), su, _p(dt), sdt, _p(a), _p(b), sb, _p(c), sc,
-                            _p(d), _p(z), sz, _p(dt_bias), _p(reset), _p(lengths), _p(saved), _p(dy), _row_stride(dy, "dy"), _p(dh_final),
+                            _p(d), _p(z), sz, _p(dt_bias), _p(reset), _p(lengths), _p(saved), _p(dy), sdy, _p(dh_final),
                             o["du"], o["ddt"], o["da"], o["db"], o["dc"], o.get("dd"), o.get("dz"), o.get("ddt_bias"), o.get("dh0"), _p(workspace),
                             _nbytes(workspace), _stream(None))
     _check(st, "ssm_scan_bwd")
@@ -315,6 +316,7 @@ def causal_conv_bwd(x, w, bias, dy, dstate_out=None, *, act="silu", state=None, 
     _conv_state(dstate_out, "dstate_out", x, width)
     _sequence_args((batch, length), reset, lengths)
     _want(dy, "dy", x.dtype, x.shape)
+    sdy = _row_stride(dy, "dy")
     workspace = _workspace(lib().ssm_conv_bwd_workspace_bytes(batch, length, d, width), workspace, x.device)
     _same_device(x, state=state, dstate_out=dstate_out, reset=reset, lengths=lengths, dy=dy, workspace=workspace)
     out = dict(dx=torch.empty(x.shape, dtype=x.dtype, device=x.device), dw=torch.empty(w.shape, dtype=_F32, device=x.device))
@@ -323,7 +325,7 @@ def causal_conv_bwd(x, w, bias, dy, dstate_out=None, *, act="silu", state=None, 
     if state is not None:
         out["dstate"] = torch.empty(state.shape, dtype=x.dtype, device=x.device)
     st = lib().ssm_conv_bwd(batch, length, d, width, _code(x.dtype), ACTS[act], _p(x), sx, _p(w), _p(bias), _p(state), _p(reset), _p(lengths), _p(dy),
-                            _row_stride(dy, "dy"), _p(dstate_out), _p(out["dx"]), _p(out["dw"]), _p(out.get("dbias")), _p(out.get("dstate")),
+                            sdy, _p(dstate_out), _p(out["dx"]), _p(out["dw"]), _p(out.get("dbias")), _p(out.get("dstate")),
                             _p(workspace), _nbytes(workspace), _stream(None))
     _check(st, "ssm_conv_bwd")
     return out
