@@ -70,8 +70,10 @@ __device__ __forceinline__ float sigmoid_of(float x) {
 
 // log(1 + e^x) and its derivative.  e^x is 2^t with the rounding of t put back; log(1 + e) is taken of the rounded
 // 1 + e and scaled by e over what that sum holds of it, so that it keeps FP32's relative precision where e is small
-// (D. Goldberg, "What every computer scientist should know about floating-point arithmetic", theorem 4).
+// (D. Goldberg, "What every computer scientist should know about floating-point arithmetic", theorem 4).  Below -110, where e^x is
+// less than FP32 holds, x counts as -110: a token masked by the lowest value or minus infinity has s = 0.
 __device__ __forceinline__ float softplus_of(float x, float* slope) {
+    x = x < -110.0f ? -110.0f : x;
     const float t = x * LOG2E, rest = fmaf(x, LOG2E, -t) + x * LOG2E_LO;
     float e = __builtin_amdgcn_exp2f(t);
     e = fmaf(e * LN2, rest, e);

@@ -123,6 +123,27 @@ def test_nothing_crosses_a_start_or_comes_from_padding():
 
 
 @pytest.mark.parametrize("dtype", [bf, f32], ids=["bf16", "f32"])
+def test_steps_of_extreme_size(dtype):
+    """A step masked by the type's lowest value or minus infinity leaves the state as it is; a large one forgets all of it, an
+    infinite one's token is not finite, and nothing of it is left behind the next start."""
+    say(f"[ssm] extreme steps {dtype}")
+    k, dy, dh = inputs(2, 40, 30, 16, 1, dtype, seed=70)
+    k["dt"][:, 5] = torch.finfo(dtype).min
+    k["dt"][:, 11:14] = float("-inf")
+    k["dt"][0, 20] = -120.0
+    k["dt"][1, 21] = -95.0
+    k["dt"][:, 25] = 300.0
+    check(run(k, dy, dh), k, dy, dh, {}, dtype, 40)
+    state = k["h0"].clone()
+    ssm.ssm_scan_step(state, *[k[n] if n in ("a", "d", "dt_bias") else k[n][:, 12] for n in ("u", "dt", "a", "b", "c", "d", "z", "dt_bias")])
+    assert torch.equal(state, k["h0"])
+    k["dt"][:, 30] = float("inf")
+    kw = dict(reset=torch.zeros(2, 40, dtype=torch.uint8, device="cuda"))
+    kw["reset"][:, 33] = 1
+    assert run(k, dy, dh, **kw)["y"][:, 33:].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", [bf, f32], ids=["bf16", "f32"])
 def test_rows_that_lie_apart(dtype):
     """Parts of wider projections, at offsets of one element, and expanded rows."""
     say(f"[ssm] strides {dtype}")
