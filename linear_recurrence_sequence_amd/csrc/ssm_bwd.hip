@@ -6,11 +6,15 @@
 //   dc = sum_i e h,  db = sum_i s u g,  da = sum_t s r,  dd = sum_t e u,
 //   dz = dy (sum_j c h + d u) (z sigmoid(z))',  dh0 = a_0 g_0.
 //
-// Bound by the vector ALU, as the forward.  From the state that the forward kept before a chunk its 16 states are formed
-// again into registers (128 of them: two channels by four states by 16 tokens a lane), then the chunk is walked from its
-// end.  Sums over states (du, ddt, dz) are in the lane but for steps over the lane groups, which four tokens share;
+// Bound by the vector ALU, as the forward.  From the state that the forward kept before a chunk of 16 tokens the states of its later
+// half are formed again into registers (64: two channels by four states by eight tokens a lane) and walked from their end, then those
+// of its earlier half.  All 16 at once would spill 136 registers; a state kept every eight tokens would double what a user keeps.
+// Sums over states (du, ddt, dz) are in the lane but for steps over the lane groups, which four tokens share;
 // sums over channels (db, dc) go through LDS: each token's eight values of a lane are summed eight lanes at a time, then over the
 // workgroup's waves, and the workgroups' parts are added by a last launch, in a fixed order.
+//
+// 32768 x 2048 channels x 16 states in BF16, gated and packed: the segments from zero 270 us, the backward 1100 to 1170 us, the last launch 19 us.
+// The vector ALU is busy for 77 and 70% of the first two's time; 256 registers and 75 KB of LDS a workgroup leave two waves a SIMD.
 #include "ssm_lay.hpp"
 
 namespace lrs {

@@ -8,6 +8,9 @@
 // so that each input is read once but for the W - 1 tokens before a piece (and behind it, backward).  The backward
 // walks the same way: the g of a token is added to the dx of the W tokens that it came from, which are stored one after
 // the other as they are complete.  A sequence's start clears what is held.
+//
+// 32768 x 2560 in BF16 with SiLU, packed: forward 64 us, 5.3 TB/s; backward 126 us, 4.0 TB/s, and 13 us for the sums (a copy of the same input takes 60 us, a sum of
+// two tensors 86).  Four channels a lane forward, two backward, whose sums and cotangents would else take 200 registers (235 us).
 #include "lm.hpp"
 #include "ssm_lay.hpp"
 

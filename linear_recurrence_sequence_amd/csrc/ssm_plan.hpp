@@ -34,14 +34,16 @@ struct SsmPlan {
 
 // The recurrence runs through a row.  Rows and channels alone are too few waves where a batch is small, so a row
 // is cut into segments: each is first run from a zero state (half of the work again), then from the state that the
-// segments before it leave.  Waves in all, and microseconds of both launches, 16 states, BF16 with a gate:
-//                            1024       2048       3072       4096       6144
+// segments before it leave.  Waves a SIMD, and microseconds of both launches, 16 states, BF16 with a gate:
+//                            1          2          3          4          6
 //   4 x 1024 x 2048          45 + 80    36 + 54    38 + 56    35 + 61    39 + 65
 //   2 x 2048 x 2048          45 + 89    36 + 60    39 + 59    35 + 71    39 + 82
 //   1 x 32768 x 2048         330 + 644  260 + 383  249 + 362  241 + 372  240 + 368
 // More waves hide more, until each walks so few tokens that going through the segments before it (one state read for
-// each) costs more: 3072, one round of what fits the chip, where that leaves 256 tokens or more to each, else 2048.  The backward's
-// registers and LDS leave room for 2048: 2 x 2048 x 2048 with 1024, 2048 and 4096 waves 47 + 248, 40 + 173 and 39 + 187.
+// each) costs more: three, which is what fits at once, where that leaves 256 tokens or more to each, else two.  The backward's
+// registers and LDS leave room for two: 2 x 2048 x 2048 with one, two and four 47 + 248, 40 + 173 and 39 + 187.
+constexpr int64_t SIMDS = 1024;
+
 inline SsmPlan ssm_plan(int64_t batch, int64_t length, int d, int n, int groups, bool backward) {
     SsmPlan p{};
     p.ng = ssm_state_groups(n);
@@ -50,7 +52,7 @@ inline SsmPlan ssm_plan(int64_t batch, int64_t length, int d, int n, int groups,
     p.blocks = (int)ceil_div(p.tiles, p.waves);
     p.chunks = (int)ceil_div(length, SSM_TOK);
     const int64_t units = std::max<int64_t>(1, batch * groups * (backward ? (int64_t)p.blocks * p.waves : p.tiles));
-    const int64_t want = !backward && p.chunks / std::max<int64_t>(1, 3072 / units) >= 256 / SSM_TOK ? 3072 : 2048;
+    const int64_t want = SIMDS * (!backward && p.chunks / std::max<int64_t>(1, 3 * SIMDS / units) >= 256 / SSM_TOK ? 3 : 2);
     const int64_t s = std::max<int64_t>(1, std::min<int64_t>({want / units, 64, p.chunks}));
     p.seg = (int)ceil_div(std::max(1, p.chunks), s);
     p.segments = (int)ceil_div(std::max(1, p.chunks), p.seg);
