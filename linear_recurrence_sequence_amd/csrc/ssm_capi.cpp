@@ -13,6 +13,7 @@ namespace lrs {
 namespace {
 
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
+static_assert(SSM_CHUNK == SSM_TOK && SSM_MAX_STATE == SSM_MOST_N, "the header's limits");
 
 scan_status check_strides(const char* fn, std::initializer_list<int64_t> strides, int64_t most = kMaxStride) {
     for (int64_t s : strides)

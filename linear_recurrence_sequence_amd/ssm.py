@@ -29,7 +29,7 @@ _BF16, _F32 = torch.bfloat16, torch.float32
 _DTYPES = (_BF16, _F32)
 _FLAGS = (torch.uint8, torch.bool)
 ACTS = {"none": 0, "silu": 1}
-MAX_STATE, MAX_WIDTH, CHUNK = 64, 4, 16
+MAX_STATE, MAX_WIDTH = 64, 4
 
 _lib = None
 
