@@ -131,10 +131,10 @@ __device__ __forceinline__ void store_pair(char* base, uint32_t off, float2 v, b
 }
 
 // ------------------------------------------------- sums over lane groups ---
-// The value of the lane whose number differs in bit M (of a row of 16 lanes; M = 4: of lanes that hold what their quad's others do).
+// The value of the lane whose number differs in bit M.
 template <int M>
 __device__ __forceinline__ float row_xor(float v) {
-    constexpr int ctrl = M == 1 ? 0xb1 : M == 2 ? 0x4e : M == 4 ? 0x141 : 0x128;  // quad [1,0,3,2], [2,3,0,1]; mirror of 8; rotation by 8
+    constexpr int ctrl = M == 1 ? 0xb1 : M == 2 ? 0x4e : 0x128;  // quad [1,0,3,2], [2,3,0,1]; rotation of 16 by 8
     return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), ctrl, 0xf, 0xf, true));
 }
 
@@ -157,23 +157,19 @@ __device__ __forceinline__ float pair_sum(float a, float b) {
 // v[i] of each of NG tokens to the sum over the NG lane groups: group g gets token g's.
 template <int NG>
 __device__ __forceinline__ float group_sum(const float (&v)[NG]) {
-    if constexpr (NG == 1) {
-        return v[0];
+    float w[NG / 2];
+    // the groups' highest bit chooses between the tokens' halves
+#pragma unroll
+    for (int i = 0; i < NG / 2; ++i) w[i] = pair_sum<32>(v[i], v[i + NG / 2]);
+    if constexpr (NG == 2) {
+        return w[0];
     } else {
-        float w[NG / 2];
-        // the groups' highest bit chooses between the tokens' halves
+        float x[NG / 4];
 #pragma unroll
-        for (int i = 0; i < NG / 2; ++i) w[i] = pair_sum<32>(v[i], v[i + NG / 2]);
-        if constexpr (NG == 2) {
-            return w[0];
-        } else {
-            float x[NG / 4];
-#pragma unroll
-            for (int i = 0; i < NG / 4; ++i) x[i] = pair_sum<16>(w[i], w[i + NG / 4]);
-            if constexpr (NG == 4) return x[0];
-            if constexpr (NG == 8) return pair_sum<8>(x[0], x[1]);
-            if constexpr (NG == 16) return pair_sum<4>(pair_sum<8>(x[0], x[2]), pair_sum<8>(x[1], x[3]));
-        }
+        for (int i = 0; i < NG / 4; ++i) x[i] = pair_sum<16>(w[i], w[i + NG / 4]);
+        if constexpr (NG == 4) return x[0];
+        if constexpr (NG == 8) return pair_sum<8>(x[0], x[1]);
+        if constexpr (NG == 16) return pair_sum<4>(pair_sum<8>(x[0], x[2]), pair_sum<8>(x[1], x[3]));
     }
 }
 

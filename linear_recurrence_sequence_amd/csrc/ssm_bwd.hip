@@ -289,7 +289,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const SsmArgs a)
                         float w = l + u;
                         if constexpr (NG <= 4) w += row_xor<1>(w);
                         if constexpr (NG <= 2) w += row_xor<2>(w);
-                        if constexpr (NG <= 1) w += row_xor<4>(w);
                         if ((lane & 7) % (8 / NG) == 0) to[(lane & 7) * NG / 8] = w;
                     }
                 };
@@ -422,7 +421,7 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(const SsmArgs a, unsigned
 
 template <class T, int NG, bool GATE>
 void launch_gate(const SsmArgs& a, hipStream_t s) {
-    constexpr int WAVES = NG == 1 ? 2 : 4;
+    constexpr int WAVES = 4;
     if (a.plan.segments > 1)
         LRS_LAUNCH(K_SSM_REV, (ssm_rev_kernel<T, NG, GATE>),
                    dim3((unsigned)ceil_div((int64_t)a.plan.tiles * a.groups * a.batch * (a.plan.segments - 1), 4)), dim3(256), 0, s, a);
@@ -438,7 +437,6 @@ template <class T>
 void launch_bwd_any(const SsmArgs& a, hipStream_t s) {
     if (a.batch > 0) {
         switch (a.plan.ng) {
-            case 1: launch_bwd<T, 1>(a, s); break;
             case 2: launch_bwd<T, 2>(a, s); break;
             case 4: launch_bwd<T, 4>(a, s); break;
             case 8: launch_bwd<T, 8>(a, s); break;

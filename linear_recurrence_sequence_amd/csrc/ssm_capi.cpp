@@ -198,7 +198,7 @@ scan_status ssm_scan_step(int64_t batch, int d, int n, int groups, int dtype, in
     if (st == SCAN_OK) st = check_alias({au, at, aa, ab, ac, as, az, ai}, {oh, oy});
     if (st != SCAN_OK) return st;
     SsmArgs k{};
-    k.plan.ng = ssm_state_groups(n);
+    k.plan.ng = n <= SSM_STATES ? 1 : ssm_state_groups(n);  // lanes of a channel
     k.batch = (int)batch, k.length = 1, k.d = d, k.n = n, k.groups = groups, k.per = d / groups, k.softplus = softplus != 0;
     k.u = u, k.dt = dt, k.b = b, k.c = c, k.z = z;
     k.u_stride = u_stride, k.dt_stride = dt_stride, k.b_stride = b_stride, k.c_stride = c_stride, k.z_stride = z_stride;

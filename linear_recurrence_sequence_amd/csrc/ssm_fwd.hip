@@ -239,7 +239,6 @@ void launch_fwd(const SsmArgs& a, hipStream_t s) {
 template <class T>
 void launch_fwd_any(const SsmArgs& a, hipStream_t s) {
     switch (a.plan.ng) {
-        case 1: return launch_fwd<T, 1>(a, s);
         case 2: return launch_fwd<T, 2>(a, s);
         case 4: return launch_fwd<T, 4>(a, s);
         case 8: return launch_fwd<T, 8>(a, s);

@@ -16,9 +16,10 @@ constexpr int SSM_MOST_N = 64;
 constexpr int64_t SSM_MOST_STRIDE = (1 << 22) - 1;  // a chunk's rows are addressed by 24-bit products and 32-bit offsets
 
 // A wave takes 128 / ng channels and all states: its lanes are ng groups (of
-// SSM_STATES states each) of 64 / ng channel pairs.
+// SSM_STATES states each) of 64 / ng channel pairs.  Two groups at least: up to four states on one group take 80 and 249 us
+// forward and backward (2 x 2048 x 2048, BF16), five on two groups 75 and 172.
 inline int ssm_state_groups(int n) {
-    int ng = 1;
+    int ng = 2;
     while (ng * SSM_STATES < n) ng *= 2;
     return ng;
 }
@@ -26,7 +27,7 @@ inline int ssm_state_groups(int n) {
 struct SsmPlan {
     int ng;               // state groups of a wave
     int tiles;            // waves over the channels of one group of b and c
-    int waves;            // waves of a workgroup (in the backward they share one group's tiles)
+    int waves;            // waves of a workgroup (in the backward they share one group of b and c)
     int blocks;           // backward: workgroups over the channels of one group of b and c
     int chunks;           // of a row
     int segments, seg;    // parts of a row worked on at once, chunks of each
@@ -47,7 +48,7 @@ constexpr int64_t SIMDS = 1024;
 inline SsmPlan ssm_plan(int64_t batch, int64_t length, int d, int n, int groups, bool backward) {
     SsmPlan p{};
     p.ng = ssm_state_groups(n);
-    p.waves = p.ng == 1 && backward ? 2 : 4;
+    p.waves = 4;
     p.tiles = (int)ceil_div(d / groups, 128 / p.ng);
     p.blocks = (int)ceil_div(p.tiles, p.waves);
     p.chunks = (int)ceil_div(length, SSM_TOK);

@@ -19,7 +19,7 @@ static void fail(const char* what, long long b, long long l, int d, int n, int g
 static void walk(int64_t b, int64_t l, int d, int n, int g) {
     for (const bool bwd : {false, true}) {
         const SsmPlan p = ssm_plan(b, l, d, n, g, bwd);
-        if (p.ng < 1 || p.ng > 16 || p.ng * SSM_STATES < n || (p.ng > 1 && p.ng / 2 * SSM_STATES >= n)) fail("state groups", b, l, d, n, g);
+        if (p.ng < 2 || p.ng > 16 || p.ng * SSM_STATES < n || (p.ng > 2 && p.ng / 2 * SSM_STATES >= n)) fail("state groups", b, l, d, n, g);
         const int64_t per = d / g, ch = 128 / p.ng;
         if (p.tiles * ch < per || (p.tiles - 1) * ch >= per) fail("tiles", b, l, d, n, g);
         if ((int64_t)p.blocks * p.waves < p.tiles || (int64_t)(p.blocks - 1) * p.waves >= p.tiles) fail("blocks", b, l, d, n, g);
