@@ -379,29 +379,27 @@ __global__ __launch_bounds__(64 * WAVES, 2) void ssm_bwd_kernel(const SsmArgs a)
 }
 
 // Sums of the workgroups' parts, in a fixed order: db and dc over the channels' workgroups (FP32, as they are few), da, dskip
-// and ddt_bias over rows and segments (FP64).  The first `bc` workgroups take db and dc.
+// and ddt_bias over rows and segments (FP64).  `x`: the first's number, or the second's.
 template <class T>
-__global__ __launch_bounds__(256) void ssm_join_kernel(const SsmArgs a, unsigned bc) {
+__device__ __forceinline__ void join_narrow(const SsmArgs& a, int64_t x) {
     const int n4 = SSM_STATES * a.plan.ng;
-    if (blockIdx.x < bc) {
-        const int64_t rows = (int64_t)a.batch * a.length, x = (int64_t)blockIdx.x * 256 + threadIdx.x;
-        if (x >= rows * a.groups * 2 * n4) return;
-        const int n = (int)(x % n4), k = (int)(x / n4 % 2), gr = (int)(x / (2 * n4) / rows);
-        const int64_t row = x / (2 * n4) % rows;
-        if (n >= a.n) return;
-        const float* at = a.part_bc + ((int64_t)gr * a.plan.blocks * rows + row) * 2 * n4 + k * n4 + n;
-        float w = 0.0f;
-        for (int i0 = 0; i0 < a.plan.blocks; i0 += 8) {
-            float v[8];
+    const int64_t rows = (int64_t)a.batch * a.length;
+    if (x >= rows * a.groups * 2 * n4) return;
+    const int n = (int)(x % n4), k = (int)(x / n4 % 2), gr = (int)(x / (2 * n4) / rows);
+    const int64_t row = x / (2 * n4) % rows;
+    if (n >= a.n) return;
+    const float* at = a.part_bc + ((int64_t)gr * a.plan.blocks * rows + row) * 2 * n4 + k * n4 + n;
+    float w = 0.0f;
+    for (int i0 = 0; i0 < a.plan.blocks; i0 += 8) {
+        float v[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = at[(int64_t)min(i0 + u, a.plan.blocks - 1) * rows * 2 * n4];
+        for (int u = 0; u < 8; ++u) v[u] = at[(int64_t)min(i0 + u, a.plan.blocks - 1) * rows * 2 * n4];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) w += i0 + u < a.plan.blocks ? v[u] : 0.0f;
-        }
-        store_value(static_cast<T*>(k ? a.db : a.dc) + (row * a.groups + gr) * a.n + n, w);
-        return;
+        for (int u = 0; u < 8; ++u) w += i0 + u < a.plan.blocks ? v[u] : 0.0f;
     }
-    const int64_t x = (int64_t)(blockIdx.x - bc) * 256 + threadIdx.x;
+    store_value(static_cast<T*>(k ? a.db : a.dc) + (row * a.groups + gr) * a.n + n, w);
+}
+__device__ __forceinline__ void join_channel(const SsmArgs& a, int64_t x) {
     const int i = (int)(x % a.d), n = (int)(x / a.d), parts = a.batch * a.plan.segments;
     if (n >= a.n + 2) return;
     const bool rate = n < a.n;
@@ -417,6 +415,13 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(const SsmArgs a, unsigned
     }
     float* out = rate ? a.da + (int64_t)i * a.n + n : n == a.n ? (a.dskip ? a.dskip + i : nullptr) : (a.ddt_bias ? a.ddt_bias + i : nullptr);
     if (out) *out = (float)w;
+}
+template <class T>
+__global__ __launch_bounds__(256) void ssm_join_kernel(const SsmArgs a, const SsmJoin j) {
+    for (int64_t w = blockIdx.x; w < j.all; w += j.grid) {
+        if (w < j.narrow) join_narrow<T>(a, w * 256 + threadIdx.x);
+        else join_channel(a, (w - j.narrow) * 256 + threadIdx.x);
+    }
 }
 
 template <class T, int NG, bool GATE>
@@ -443,8 +448,8 @@ void launch_bwd_any(const SsmArgs& a, hipStream_t s) {
             default: launch_bwd<T, 16>(a, s);
         }
     }
-    const unsigned bc = (unsigned)ceil_div((int64_t)a.batch * a.length * a.groups * 2 * SSM_STATES * a.plan.ng, 256);
-    LRS_LAUNCH(K_SSM_JOIN, (ssm_join_kernel<T>), dim3(bc + (unsigned)ceil_div((int64_t)a.d * (a.n + 2), 256)), dim3(256), 0, s, a, bc);
+    const SsmJoin j = ssm_join(a.batch, a.length, a.d, a.n, a.groups, a.plan.ng);
+    LRS_LAUNCH(K_SSM_JOIN, (ssm_join_kernel<T>), dim3(j.grid), dim3(256), 0, s, a, j);
 }
 
 }  // namespace

@@ -65,6 +65,20 @@ inline bool ssm_shape(int64_t batch, int64_t length, int d, int n, int groups) {
            d >= 1 && d <= (1 << 21) && groups >= 1 && d % groups == 0 && n >= 1 && n <= SSM_MOST_N;
 }
 
+// The backward's last launch: workgroups of 256 sums, first of db and dc (two values for each row, group and padded state), then of da, dskip and
+// ddt_bias (n + 2 for each channel).  Together they may need more threads than a launch has, so that a workgroup of the grid takes every grid-th.
+struct SsmJoin {
+    int64_t narrow, all;  // workgroups of db and dc, and of everything
+    unsigned grid;
+};
+inline SsmJoin ssm_join(int64_t batch, int64_t length, int d, int n, int groups, int ng) {
+    SsmJoin j{};
+    j.narrow = ceil_div(batch * length * groups * 2 * SSM_STATES * ng, 256);
+    j.all = j.narrow + ceil_div((int64_t)d * (n + 2), 256);
+    j.grid = (unsigned)std::min<int64_t>(j.all, MOST_THREADS / 256);
+    return j;
+}
+
 // Sizes that the launches cover: workgroups of 256 threads, and element counts within 62 bits.
 inline bool ssm_fits(int64_t batch, int64_t length, int d, int n, int groups) {
     if (!ssm_shape(batch, length, d, n, groups)) return false;

@@ -1,0 +1,39 @@
+"""The selective scan at its widest accepted sizes on the GPU."""
+import pytest
+import torch
+
+from linear_recurrence_sequence_amd import ssm
+from tests.helpers import say
+from tests.ssm_ref import U, scan_ref, scan_tolerance
+
+pytestmark = pytest.mark.gpu
+bf, f32 = torch.bfloat16, torch.float32
+
+
+def test_a_last_launch_of_more_than_2_32_threads():
+    """batch * length just below 2^25 with more than 32 states: db and dc alone take 2^32 threads but for a few.  Every row holds the
+    same tokens, so that one row in 64 bits says what all of them hold; da adds the rows up in FP64 and rounds once more."""
+    batch, length, n = 20485, 1638, 33
+    say(f"[ssm] batch={batch} length={length} d=1 n={n}")
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device="cuda")
+
+    one = dict(u=normal(1, length, 1).to(bf), dt=normal(1, length, 1).to(bf), a=-torch.rand(1, n, generator=g, device="cuda") - 0.1,
+               b=normal(1, length, 1, n).to(bf), c=normal(1, length, 1, n).to(bf), d=normal(1), dt_bias=normal(1) - 2)
+    dy = normal(1, length, 1).to(bf)
+    k = {m: t.repeat(batch, *[1] * (t.dim() - 1)) if m in ("u", "dt", "b", "c") else t for m, t in one.items()}
+    y, h, saved = ssm.ssm_scan_fwd(**k)
+    got = ssm.ssm_scan_bwd(k["u"], k["dt"], k["a"], k["b"], k["c"], k["d"], None, k["dt_bias"], saved, dy.repeat(batch, 1, 1))
+    torch.cuda.synchronize()
+    got.update(y=y, h=h)
+    ref = scan_ref(**one, dy=dy)
+    tol = scan_tolerance(scan_ref(**one, dy=dy, absolute=True), ref, length, bf)
+    for m, t in got.items():
+        if m in ("da", "dd", "ddt_bias"):
+            err, most = (t.double() - batch * ref[m]).abs(), batch * (tol[m] + U * ref[m].abs())
+        else:
+            assert (t == t[:1]).all(), m
+            err, most = (t[:1].double() - ref[m]).abs(), tol[m]
+        assert (err <= most).all(), (m, float(err.max()))
