@@ -142,8 +142,9 @@ scan_status lm_adamw_step(int count, int param_dtype, int grad_dtype, int state_
  * vocabulary's rows w [v, d].  A negative token is padding: its row of out is
  * zero, and it has no gradient.  A token >= v: its row is NaN, without one either.
  * Products are FP32, out is rounded once (where it is BF16).
- * 1 <= d <= 2^23, 1 <= v < 2^31 - 256, 0 <= n <= 2^26 - 64.
+ * 1 <= d <= 2^23, 1 <= v <= LM_EMBED_MAX_V, 0 <= n <= 2^26 - 64.
  * ====================================================================== */
+#define LM_EMBED_MAX_V 2147483136 /* (2^22 - 1) * 512 */
 
 /* Forward.  w [v, d] of w_dtype and out [n, d] of out_dtype, dense. */
 scan_status lm_embed_fwd(int64_t n, int d, int64_t v, int w_dtype, int out_dtype, double scale, const int64_t* tokens,

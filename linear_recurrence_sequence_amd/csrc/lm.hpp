@@ -182,6 +182,9 @@ hipError_t launch_ce_bwd(const CeArgs& a, hipStream_t s);
 
 // ------------------------------------------------------ embedding lookup ---
 constexpr int EMBED_ROWS = 512;   // rows of the vocabulary that a sorting workgroup takes
+constexpr int EMBED_WAVES = 16;   // of a sorting workgroup
+// The sort is the launch with the most threads for a row, two, in whole workgroups.
+constexpr int64_t EMBED_MOST_V = MOST_THREADS / (64 * EMBED_WAVES) * EMBED_ROWS;
 constexpr int EMBED_RUN = 32;     // tokens that one wave adds up for a row
 struct EmbedArgs {
     int64_t n, v;                 // tokens, rows of the vocabulary

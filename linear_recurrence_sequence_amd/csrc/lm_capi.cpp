@@ -79,13 +79,14 @@ scan_status ce_check(const char* fn, int64_t n, int d, int64_t v, double cap, in
     return SCAN_OK;
 }
 
-// Launches of up to 64 threads for a token or a row of the vocabulary along x, and a workgroup for 256 columns along y.
+static_assert(LM_EMBED_MAX_V == EMBED_MOST_V, "the header's limit");
+// Launches of 64 threads for a token, or two for a row of the vocabulary in whole workgroups, along x, and a workgroup for 256 columns along y.
 bool embed_shape(int64_t n, int d, int64_t v) {
-    return n >= 0 && d >= 1 && v >= 1 && n <= (1 << 26) - 64 && v <= 0x7fffff00 && d <= (1 << 23);
+    return n >= 0 && d >= 1 && v >= 1 && n <= (1 << 26) - 64 && v <= EMBED_MOST_V && d <= (1 << 23);
 }
 scan_status embed_refuse(const char* fn, int64_t n, int d, int64_t v) {
     return fail(SCAN_ERR_SHAPE, std::string(fn) + ": unsupported shape n=" + std::to_string(n) + " d=" + std::to_string(d) + " v=" +
-                                    std::to_string(v) + " (need 1 <= d <= 2^23, 1 <= v < 2^31 - 256, n <= 2^26 - 64)");
+                                    std::to_string(v) + " (need 1 <= d <= 2^23, 1 <= v <= " + std::to_string(EMBED_MOST_V) + ", n <= 2^26 - 64)");
 }
 
 // The gradient's buffers inside the caller's workspace (base NULL: sizes only).

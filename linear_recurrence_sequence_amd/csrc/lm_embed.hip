@@ -16,8 +16,6 @@
 namespace lrs {
 namespace {
 
-constexpr int WAVES = 16;  // of a sorting workgroup
-
 constexpr int BATCH = 4;   // groups of 256 columns (and tokens, in the gradient) whose loads of a wave are in flight together
 
 // A wave takes BATCH * 256 columns of a token.
@@ -44,7 +42,8 @@ __global__ __launch_bounds__(256) void embed_fwd_kernel(const EmbedArgs a) {
     }
 }
 
-__global__ __launch_bounds__(64 * WAVES) void embed_sort_kernel(const EmbedArgs a) {
+__global__ __launch_bounds__(64 * EMBED_WAVES) void embed_sort_kernel(const EmbedArgs a) {
+    constexpr int WAVES = EMBED_WAVES;
     __shared__ int count[WAVES][EMBED_ROWS];  // a wave's tokens of each row, then where its next one of that row goes
     __shared__ int below[WAVES], sums[WAVES];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -268,7 +267,7 @@ template <class OT, class GT, bool TAIL>
 void launch_grad(const EmbedArgs& a, hipStream_t s) {
     const int64_t runs = ceil_div(a.n, EMBED_RUN);
     const unsigned of_runs = (unsigned)ceil_div(runs, 4);
-    if (a.n > 0) LRS_LAUNCH(K_LM_EMBED_SORT, embed_sort_kernel, dim3((unsigned)ceil_div(a.v, EMBED_ROWS)), dim3(64 * WAVES), 0, s, a);
+    if (a.n > 0) LRS_LAUNCH(K_LM_EMBED_SORT, embed_sort_kernel, dim3((unsigned)ceil_div(a.v, EMBED_ROWS)), dim3(64 * EMBED_WAVES), 0, s, a);
     // 32768 tokens x 2048, vocabulary 128000: 2048, 4096, 8192, 16384 and all 32000 workgroups take 160, 149, 146, 140 and 139 us
     const unsigned of_rows = (unsigned)std::min<int64_t>(ceil_div(a.v, 4), 16384);
     LRS_LAUNCH(K_LM_EMBED_GRAD, (embed_grad_kernel<OT, GT, TAIL>), dim3(of_runs + of_rows), dim3(256), 0, s, a, of_runs, (int)of_rows * 4);
