@@ -144,9 +144,12 @@ def _want(t, name, dtypes, shape=None, optional=False):
 
 
 def _want_bytes(t, name, need):
-    """A caller-provided byte buffer (saved record, workspace) of at least `need` bytes."""
+    """A caller-provided byte buffer (saved record, workspace) of at least `need` bytes,
+    one after the other."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     if need == 0:
         raise ValueError(f"{name}: unsupported shape (the size query returned 0)")
     if _nbytes(t) < need:
