@@ -230,7 +230,7 @@ def block_norm_bwd(x, y, gate, w_post, scale, w_pre, stats, dr, dn, *, eps=1e-6,
     need = lib().lm_block_norm_bwd_workspace_bytes(rows, d)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _want_bytes(workspace, "workspace", need)
+    _want_bytes(workspace, "workspace", need, dev)
     st = lib().lm_block_norm_bwd(rows, d, _code(x.dtype), _code(y.dtype), GATES[gate_act], _p(x), sx,
                                  _p(y), sy, _p(gate), sg, _p(w_post), _p(scale), _p(w_pre), _p(stats), _p(dr),
                                  _row_stride(dr, "dr"), _p(dn), _row_stride(dn, "dn"), _p(out["dx"]), _p(out["dy"]),
@@ -259,7 +259,7 @@ def _ce_workspace(n, d, v, backward, workspace, dev):
         raise ValueError(f"unsupported shape: {n} tokens, width {d}, vocabulary {v} (the width must be a multiple of 8 in 8..65536)")
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=dev)
-    _want_bytes(workspace, "workspace", need)
+    _want_bytes(workspace, "workspace", need, dev)
     return workspace
 
 
@@ -498,7 +498,7 @@ def embed_bwd(tokens, dout, v, *, scale=1.0, grad_dtype=_BF16, dw=None, accumula
         raise ValueError(f"unsupported shape: {n} tokens, width {d}, vocabulary {v}")
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dout.device)
-    _want_bytes(workspace, "workspace", need)
+    _want_bytes(workspace, "workspace", need, dout.device)
     st = lib().lm_embed_bwd(n, d, v, _code(dout.dtype), _code(dw.dtype), scale, _p(tokens), _p(dout), sg, int(bool(accumulate)),
                             _p(dw), _p(workspace), _nbytes(workspace), _stream(None))
     _check(st, "lm_embed_bwd")

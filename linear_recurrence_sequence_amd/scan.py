@@ -143,11 +143,13 @@ def _want(t, name, dtypes, shape=None, optional=False):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _want_bytes(t, name, need):
+def _want_bytes(t, name, need, device=None):
     """A caller-provided byte buffer (saved record, workspace) of at least `need` bytes,
-    one after the other."""
+    one after the other (on `device`, where one is given)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if need == 0:

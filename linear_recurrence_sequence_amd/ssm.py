@@ -118,7 +118,7 @@ def _workspace(need, workspace, device):
         raise ValueError("unsupported shape: batch * length must stay below 2^31 and a launch below 2^32 threads")
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=device)
-    _want_bytes(workspace, "workspace", need)
+    _want_bytes(workspace, "workspace", need, device)
     return workspace
 
 
@@ -194,7 +194,7 @@ def ssm_scan_bwd(u, dt, a, b, c, d, z, dt_bias, saved, dy, dh_final=None, *, sof
     workspace = _workspace(need, workspace, dev)
     _want(saved, "saved", torch.uint8, (lib().ssm_scan_saved_bytes(batch, length, width, n, groups),))
     _dense(saved, "saved")
-    _same_device(u, reset=reset, lengths=lengths, dy=dy, dh_final=dh_final, saved=saved, workspace=workspace)
+    _same_device(u, reset=reset, lengths=lengths, dy=dy, dh_final=dh_final, saved=saved)
     wide, group = dict(dtype=u.dtype, device=dev), dict(dtype=_F32, device=dev)
     out = dict(du=torch.empty(u.shape, **wide), ddt=torch.empty(u.shape, **wide), da=torch.empty(a.shape, **group),
                db=torch.empty(b.shape, **wide), dc=torch.empty(b.shape, **wide))
@@ -318,7 +318,7 @@ def causal_conv_bwd(x, w, bias, dy, dstate_out=None, *, act="silu", state=None, 
     _want(dy, "dy", x.dtype, x.shape)
     sdy = _row_stride(dy, "dy")
     workspace = _workspace(lib().ssm_conv_bwd_workspace_bytes(batch, length, d, width), workspace, x.device)
-    _same_device(x, state=state, dstate_out=dstate_out, reset=reset, lengths=lengths, dy=dy, workspace=workspace)
+    _same_device(x, state=state, dstate_out=dstate_out, reset=reset, lengths=lengths, dy=dy)
     out = dict(dx=torch.empty(x.shape, dtype=x.dtype, device=x.device), dw=torch.empty(w.shape, dtype=_F32, device=x.device))
     if bias is not None:
         out["dbias"] = torch.empty(d, dtype=_F32, device=x.device)

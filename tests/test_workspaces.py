@@ -39,3 +39,9 @@ def test_a_workspace_that_is_not_dense(name):
         calls()[name](torch.zeros(2 << 20, dtype=torch.uint8)[::2])
     with pytest.raises(ValueError, match="device tensor"):
         calls()[name](torch.zeros(1 << 20, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_workspace_of_another_device(name):
+    with pytest.raises(ValueError, match="workspace is on meta, expected cpu"):
+        calls()[name](torch.empty(1 << 20, dtype=torch.uint8, device="meta"))
