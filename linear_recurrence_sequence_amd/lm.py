@@ -26,6 +26,7 @@ _BF16, _F32 = torch.bfloat16, torch.float32
 _DTYPES = (_BF16, _F32)
 GATES = {"none": 0, "sigmoid": 1, "silu": 2}
 ADAMW_BLOCK = 256
+EMBED_MAX_D = 1 << 23
 
 _lib = None
 _bound = None
@@ -441,8 +442,8 @@ def embed_fwd(tokens, w, *, scale=1.0, out_dtype=None, out=None, stream=None):
             _check(r, "lm_embed_fwd")
     _want(tokens, "tokens", torch.int64)
     _want(w, "w", _DTYPES)
-    if w.dim() != 2 or w.shape[0] < 1 or w.shape[1] < 1:
-        raise ValueError(f"w must be [v, d] with v, d >= 1, got shape {tuple(w.shape)}")
+    if w.dim() != 2 or w.shape[0] < 1 or not 1 <= w.shape[1] <= EMBED_MAX_D:
+        raise ValueError(f"w must be [v, d] with v >= 1 and d from 1 up to {EMBED_MAX_D}, got shape {tuple(w.shape)}")
     _dense(tokens, "tokens")
     _dense(w, "w")
     v, d = w.shape
@@ -478,8 +479,9 @@ def embed_bwd(tokens, dout, v, *, scale=1.0, grad_dtype=_BF16, dw=None, accumula
             _check(r, "lm_embed_bwd")
     _want(tokens, "tokens", torch.int64)
     _want(dout, "dout", _DTYPES)
-    if dout.dim() < 1 or dout.shape[:-1] != tokens.shape or dout.shape[-1] < 1:
-        raise ValueError(f"dout must be [..., d] with the tokens' shape in front, got shapes {tuple(dout.shape)} and {tuple(tokens.shape)}")
+    if dout.dim() < 1 or dout.shape[:-1] != tokens.shape or not 1 <= dout.shape[-1] <= EMBED_MAX_D:
+        raise ValueError(f"dout must be [..., d] with the tokens' shape in front and d from 1 up to {EMBED_MAX_D}, "
+                         f"got shapes {tuple(dout.shape)} and {tuple(tokens.shape)}")
     _dense(tokens, "tokens")
     n, d, v, sg = tokens.numel(), dout.shape[-1], int(v), _row_stride(dout, "dout")
     if accumulate and dw is None:

@@ -30,6 +30,7 @@ _DTYPES = (_BF16, _F32)
 _FLAGS = (torch.uint8, torch.bool)
 ACTS = {"none": 0, "silu": 1}
 MAX_STATE, MAX_WIDTH = 64, 4
+MAX_SCAN_D, MAX_CONV_D = 1 << 21, 1 << 24
 
 _lib = None
 
@@ -92,8 +93,8 @@ def _sequence_args(lead, reset, lengths):
 def _scan_args(u, dt, a, b, c, d, z, dt_bias, dims):
     """Checks what all calls of the scan share; returns (d, n, groups, row strides of u, dt, b, c, z)."""
     _want(u, "u", _DTYPES)
-    if u.dim() != dims or u.shape[-1] < 1:
-        raise ValueError(f"u must be [batch{', length' if dims == 3 else ''}, d] with d >= 1, got shape {tuple(u.shape)}")
+    if u.dim() != dims or not 1 <= u.shape[-1] <= MAX_SCAN_D:
+        raise ValueError(f"u must be [batch{', length' if dims == 3 else ''}, d] with d from 1 up to {MAX_SCAN_D}, got shape {tuple(u.shape)}")
     lead, width = u.shape[:-1], u.shape[-1]
     _want(dt, "dt", u.dtype, u.shape)
     _want(z, "z", u.dtype, u.shape, optional=True)
@@ -247,8 +248,8 @@ def _conv_args(x, w, bias, act, dims):
     if act not in ACTS:
         raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
     _want(x, "x", _DTYPES)
-    if x.dim() != dims or x.shape[-1] < 1:
-        raise ValueError(f"x must be [batch{', length' if dims == 3 else ''}, d] with d >= 1, got shape {tuple(x.shape)}")
+    if x.dim() != dims or not 1 <= x.shape[-1] <= MAX_CONV_D:
+        raise ValueError(f"x must be [batch{', length' if dims == 3 else ''}, d] with d from 1 up to {MAX_CONV_D}, got shape {tuple(x.shape)}")
     d = x.shape[-1]
     _want(w, "w", _F32)
     if w.dim() != 2 or w.shape[0] != d or not 2 <= w.shape[1] <= MAX_WIDTH:
