@@ -127,7 +127,11 @@ __device__ __forceinline__ float2 load_two(const SsmArgs& a, const float* v, con
     return make_float2(v[p.odd ? last : p.i], v[last]);
 }
 
-// What a segment from nothing leaves: the product of its decays (0 behind a sequence's start) and its state or cotangent.
+// Stands for the product of a segment's decays where a sequence starts in it: nothing crosses that, whatever it was.  A product that is 0
+// because FP32 holds no less is another matter: what is not finite stays so.
+constexpr float SEGMENT_STARTS = -1.0f;
+
+// What a segment from nothing leaves: the product of its decays and its state or cotangent.
 template <int NG>
 __device__ __forceinline__ void put_segment(const SsmArgs& a, const Place& p, const float (&A)[2][4], const bool (&okn)[4], float2 total,
                                             bool anew, const float (&h)[2][4]) {
@@ -141,14 +145,13 @@ __device__ __forceinline__ void put_segment(const SsmArgs& a, const Place& p, co
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
         if (!okn[s]) continue;
-        const float d0 = anew ? 0.0f : __builtin_amdgcn_exp2f(total.x * A[0][s]);
-        const float d1 = anew ? 0.0f : __builtin_amdgcn_exp2f(total.y * A[1][s]);
+        const float d0 = anew ? SEGMENT_STARTS : __builtin_amdgcn_exp2f(total.x * A[0][s]);
+        const float d1 = anew ? SEGMENT_STARTS : __builtin_amdgcn_exp2f(total.y * A[1][s]);
         store_pair<float>(at, state_off(a, 4 * p.g + s, p.c0), make_float2(d0, d1), p.ok0, p.ok1);
         store_pair<float>(at, state_off(a, a.n + 4 * p.g + s, p.c0), make_float2(h[0][s], h[1][s]), p.ok0, p.ok1);
     }
 }
-// A lane's states h through the segments from, from + step, .. up to `to` (not included), four of them on their way at a time.  A product of 0 also
-// stands for a sequence's start, behind which nothing counts, whatever it was.
+// A lane's states h through the segments from, from + step, .. up to `to` (not included), four of them on their way at a time.
 __device__ __forceinline__ void through_segments(const SsmArgs& a, const Place& p, int from, int to, int step, float (&h)[2][4]) {
     const int64_t one = (int64_t)2 * a.n * a.d;
     const int count = (to - from) * step;
@@ -172,8 +175,8 @@ __device__ __forceinline__ void through_segments(const SsmArgs& a, const Place& 
             for (int s = 0; s < 4; ++s) {
                 const float2 k = own(decay[u][s].get(), p), x = own(left[u][s].get(), p);
                 if (i0 + u < count) {
-                    h[0][s] = k.x == 0.0f ? x.x : fmaf(k.x, h[0][s], x.x);
-                    h[1][s] = k.y == 0.0f ? x.y : fmaf(k.y, h[1][s], x.y);
+                    h[0][s] = k.x == SEGMENT_STARTS ? x.x : fmaf(k.x, h[0][s], x.x);
+                    h[1][s] = k.y == SEGMENT_STARTS ? x.y : fmaf(k.y, h[1][s], x.y);
                 }
             }
     }
