@@ -127,11 +127,12 @@ __device__ __forceinline__ float2 load_two(const SsmArgs& a, const float* v, con
     return make_float2(v[p.odd ? last : p.i], v[last]);
 }
 
-// Stands for the product of a segment's decays where a sequence starts in it: nothing crosses that, whatever it was.  A product that is 0
-// because FP32 holds no less is another matter: what is not finite stays so.
+// Stands for a segment's decays where a sequence starts in it: nothing crosses that, whatever it was.  Decays too small for FP32 are
+// another matter: what is not finite stays so.
 constexpr float SEGMENT_STARTS = -1.0f;
 
-// What a segment from nothing leaves: the product of its decays and its state or cotangent.
+// What a segment from nothing leaves: the root of the product of its decays, and its state or cotangent.  The product itself may lie far beyond FP32
+// (factors above one are allowed) where the state times it does not; its root is applied twice.
 template <int NG>
 __device__ __forceinline__ void put_segment(const SsmArgs& a, const Place& p, const float (&A)[2][4], const bool (&okn)[4], float2 total,
                                             bool anew, const float (&h)[2][4]) {
@@ -145,11 +146,15 @@ __device__ __forceinline__ void put_segment(const SsmArgs& a, const Place& p, co
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
         if (!okn[s]) continue;
-        const float d0 = anew ? SEGMENT_STARTS : __builtin_amdgcn_exp2f(total.x * A[0][s]);
-        const float d1 = anew ? SEGMENT_STARTS : __builtin_amdgcn_exp2f(total.y * A[1][s]);
+        const float d0 = anew ? SEGMENT_STARTS : __builtin_amdgcn_exp2f(0.5f * total.x * A[0][s]);
+        const float d1 = anew ? SEGMENT_STARTS : __builtin_amdgcn_exp2f(0.5f * total.y * A[1][s]);
         store_pair<float>(at, state_off(a, 4 * p.g + s, p.c0), make_float2(d0, d1), p.ok0, p.ok1);
         store_pair<float>(at, state_off(a, a.n + 4 * p.g + s, p.c0), make_float2(h[0][s], h[1][s]), p.ok0, p.ok1);
     }
+}
+// A state through a segment.  One that is zero stays so, whatever the decays' product is.
+__device__ __forceinline__ float through(float root, float h, float left) {
+    return root == SEGMENT_STARTS || h == 0.0f ? left : fmaf(h * root, root, left);
 }
 // A lane's states h through the segments from, from + step, .. up to `to` (not included), four of them on their way at a time.
 __device__ __forceinline__ void through_segments(const SsmArgs& a, const Place& p, int from, int to, int step, float (&h)[2][4]) {
@@ -175,8 +180,8 @@ __device__ __forceinline__ void through_segments(const SsmArgs& a, const Place& 
             for (int s = 0; s < 4; ++s) {
                 const float2 k = own(decay[u][s].get(), p), x = own(left[u][s].get(), p);
                 if (i0 + u < count) {
-                    h[0][s] = k.x == SEGMENT_STARTS ? x.x : fmaf(k.x, h[0][s], x.x);
-                    h[1][s] = k.y == SEGMENT_STARTS ? x.y : fmaf(k.y, h[1][s], x.y);
+                    h[0][s] = through(k.x, h[0][s], x.x);
+                    h[1][s] = through(k.y, h[1][s], x.y);
                 }
             }
     }
