@@ -34,7 +34,7 @@ __device__ __forceinline__ void load_chunk(const SsmArgs& a, const Place& p, int
     const int left = a.length - chunk * SSM_TOK, g = fresh_lane() / Lay<NG>::J;
     const char *u = rows_at<T>(a.u, row0, a.u_stride), *dt = rows_at<T>(a.dt, row0, a.dt_stride), *z = rows_at<T>(a.z, row0, a.z_stride),
             *dy = rows_at<T>(a.dy, row0, a.dy_stride);
-    both_ways(a.d == 1, [&](auto one) {
+    both_ways(a.per == 1, [&](auto one) {
         constexpr bool single = decltype(one)::value;
 #pragma unroll
         for (int q = 0; q < Lay<NG>::Q; ++q) {
@@ -50,7 +50,7 @@ __device__ __forceinline__ void load_chunk(const SsmArgs& a, const Place& p, int
     if (!SUM) {
         const char* at = reinterpret_cast<const char*>(a.saved + ((int64_t)p.b * a.plan.chunks + chunk) * a.n * a.d);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) v.h[s] = Pair<float>::load(at, state_off(a, min(4 * g + s, a.n - 1), p.i), a.d == 1);
+        for (int s = 0; s < 4; ++s) v.h[s] = Pair<float>::load(at, state_off(a, min(4 * g + s, a.n - 1), p.i), a.per == 1);
     }
 }
 

@@ -30,7 +30,7 @@ __device__ __forceinline__ void load_chunk(const SsmArgs& a, const Place& p, int
     const int64_t row0 = (int64_t)p.b * a.length + chunk * SSM_TOK;
     const int left = a.length - chunk * SSM_TOK, g = fresh_lane() / Lay<NG>::J;
     const char *u = rows_at<T>(a.u, row0, a.u_stride), *dt = rows_at<T>(a.dt, row0, a.dt_stride), *z = rows_at<T>(a.z, row0, a.z_stride);
-    both_ways(a.d == 1, [&](auto single) {
+    both_ways(a.per == 1, [&](auto single) {
 #pragma unroll
         for (int q = 0; q < Lay<NG>::Q; ++q) {
             const int r = min(q * NG + g, left - 1);

@@ -32,7 +32,7 @@ __device__ __forceinline__ void both_ways(bool uniform, F f) {
 // A wave's row and segment, its lane's part of the channels and states.
 struct Place {
     int b, seg, gr, tile, c0;    // row, segment, group of b and c, tile of its channels, the lane's first channel
-    int i;                       // first of the two channels that the lane loads: its own, or existing ones
+    int i;                       // first of the two channels that the lane loads: its own, or existing ones of its group
     bool ok0, ok1, odd;          // which of its channels exist; odd: the first is the second one loaded (a group's last, without a partner)
     int g, j;                    // the lane's group of states and pair of channels
 };
@@ -44,8 +44,9 @@ __device__ __forceinline__ Place place_of(const SsmArgs& a, int tile, int gr, in
     p.g = lane / Lay<NG>::J, p.j = lane % Lay<NG>::J;
     p.c0 = gr * a.per + tile * Lay<NG>::CH + 2 * p.j;
     p.ok0 = p.c0 < end, p.ok1 = p.c0 + 1 < end;
-    p.i = max(min(p.c0, end - 2), 0);
-    p.odd = p.c0 == p.i + 1 || a.d == 1;  // of one channel in all, that one is loaded as the second
+    // Lanes without channels load their group's last ones: what those of another group hold, NaN say, must not reach this one's db and dc.
+    p.i = max(min(p.c0, end - 2), gr * a.per);
+    p.odd = p.c0 == p.i + 1 || a.per == 1;  // a group's only channel is loaded as the second
     return p;
 }
 
@@ -123,7 +124,7 @@ __device__ __forceinline__ void load_rates(const SsmArgs& a, const Place& p, flo
 // Two of a vector's values.
 __device__ __forceinline__ float2 load_two(const SsmArgs& a, const float* v, const Place& p) {
     if (!v) return make_float2(0.f, 0.f);
-    const int last = p.i + (a.d > 1 ? 1 : 0);
+    const int last = p.i + (a.per > 1 ? 1 : 0);
     return make_float2(v[p.odd ? last : p.i], v[last]);
 }
 
@@ -170,8 +171,8 @@ __device__ __forceinline__ void through_segments(const SsmArgs& a, const Place& 
             const char* at = reinterpret_cast<const char*>(a.part + ((int64_t)p.b * a.plan.segments + from + step * min(i0 + u, count - 1)) * one);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                decay[u][s] = Pair<float>::load(at, off[s], a.d == 1);
-                left[u][s] = Pair<float>::load(at + one * 2, off[s], a.d == 1);
+                decay[u][s] = Pair<float>::load(at, off[s], a.per == 1);
+                left[u][s] = Pair<float>::load(at + one * 2, off[s], a.per == 1);
             }
         }
 #pragma unroll
