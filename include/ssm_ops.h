@@ -44,7 +44,7 @@ extern "C" {
  *   dtype, a row's groups * n values dense;  a f32 [d, n];  skip (d above) and
  *   dt_bias f32 [d], NULL = 0;  h0 f32 [batch, d, n], NULL = 0.
  * batch, length >= 0, 1 <= d <= 2^21 and a multiple of groups, 1 <= n <= SSM_MAX_STATE,
- * batch * length < 2^31, row strides below 2^22.
+ * batch * length < 2^31, row strides below 2^22 (of a single token: up to 2^40).
  * ====================================================================== */
 #define SSM_MAX_STATE 64
 /* Tokens between two states that the forward keeps for the backward. */
@@ -84,7 +84,8 @@ scan_status ssm_scan_bwd(int64_t batch, int64_t length, int d, int n, int groups
                          void* dz, float* ddt_bias, float* dh0, void* workspace, size_t workspace_bytes, void* stream);
 
 /* One token of `batch` sequences: h f32 [batch, d, n], dense, is updated in place, y
- * [batch, d] of dtype, dense; the other tensors as above with length 1. */
+ * [batch, d] of dtype, dense; the other tensors as above with length 1, row strides up to 2^40 (a
+ * token's slice of longer rows). */
 scan_status ssm_scan_step(int64_t batch, int d, int n, int groups, int dtype, int softplus, float* h, const void* u,
                           int64_t u_stride, const void* dt, int64_t dt_stride, const float* a, const void* b,
                           int64_t b_stride, const void* c, int64_t c_stride, const float* skip, const void* z,

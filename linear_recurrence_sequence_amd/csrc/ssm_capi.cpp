@@ -22,14 +22,14 @@ scan_status check_strides(const char* fn, std::initializer_list<int64_t> strides
 }
 
 scan_status ssm_check(const char* fn, int64_t batch, int64_t length, int d, int n, int groups, int dtype,
-                      std::initializer_list<int64_t> strides) {
+                      std::initializer_list<int64_t> strides, int64_t most_stride) {
     if (!ssm_fits(batch, length, d, n, groups))
         return fail(SCAN_ERR_SHAPE, std::string(fn) + ": unsupported shape batch=" + std::to_string(batch) + " length=" + std::to_string(length) +
                                         " d=" + std::to_string(d) + " n=" + std::to_string(n) + " groups=" + std::to_string(groups) +
                                         " (need d a multiple of groups, 1 <= n <= " + std::to_string(SSM_MAX_STATE) +
                                         ", batch * length < 2^31 and launches below 2^32 threads)");
     if (!dtype_ok(dtype)) return fail(SCAN_ERR_SHAPE, std::string(fn) + ": dtype must be SCAN_BF16 or SCAN_F32");
-    return check_strides(fn, strides, SSM_MOST_STRIDE);
+    return check_strides(fn, strides, most_stride);
 }
 
 scan_status check_workspace(const char* fn, size_t have, size_t need) {
@@ -115,7 +115,7 @@ scan_status ssm_scan_fwd(int64_t batch, int64_t length, int d, int n, int groups
                          const void* dt, int64_t dt_stride, const float* a, const void* b, int64_t b_stride, const void* c, int64_t c_stride,
                          const float* skip, const void* z, int64_t z_stride, const float* dt_bias, const float* h0, const uint8_t* reset,
                          const int32_t* lengths, void* y, float* h_final, void* saved, void* workspace, size_t workspace_bytes, void* stream) {
-    scan_status st = ssm_check("ssm_scan_fwd", batch, length, d, n, groups, dtype, {u_stride, dt_stride, b_stride, c_stride, z_stride});
+    scan_status st = ssm_check("ssm_scan_fwd", batch, length, d, n, groups, dtype, {u_stride, dt_stride, b_stride, c_stride, z_stride}, SSM_MOST_STRIDE);
     if (st != SCAN_OK) return st;
     if (batch == 0) return SCAN_OK;
     const size_t es = dtype_size(dtype), state = (size_t)batch * d * n * 4;
@@ -148,7 +148,8 @@ scan_status ssm_scan_bwd(int64_t batch, int64_t length, int d, int n, int groups
                          const float* skip, const void* z, int64_t z_stride, const float* dt_bias, const uint8_t* reset, const int32_t* lengths,
                          const void* saved, const void* dy, int64_t dy_stride, const float* dh_final, void* du, void* ddt, float* da, void* db,
                          void* dc, float* dskip, void* dz, float* ddt_bias, float* dh0, void* workspace, size_t workspace_bytes, void* stream) {
-    scan_status st = ssm_check("ssm_scan_bwd", batch, length, d, n, groups, dtype, {u_stride, dt_stride, b_stride, c_stride, z_stride, dy_stride});
+    scan_status st = ssm_check("ssm_scan_bwd", batch, length, d, n, groups, dtype, {u_stride, dt_stride, b_stride, c_stride, z_stride, dy_stride},
+                               SSM_MOST_STRIDE);
     if (st != SCAN_OK) return st;
     const size_t es = dtype_size(dtype), state = (size_t)batch * d * n * 4;
     const int64_t rows = batch * length;
@@ -186,7 +187,7 @@ scan_status ssm_scan_bwd(int64_t batch, int64_t length, int d, int n, int groups
 scan_status ssm_scan_step(int64_t batch, int d, int n, int groups, int dtype, int softplus, float* h, const void* u, int64_t u_stride,
                           const void* dt, int64_t dt_stride, const float* a, const void* b, int64_t b_stride, const void* c, int64_t c_stride,
                           const float* skip, const void* z, int64_t z_stride, const float* dt_bias, void* y, void* stream) {
-    scan_status st = ssm_check("ssm_scan_step", batch, 1, d, n, groups, dtype, {u_stride, dt_stride, b_stride, c_stride, z_stride});
+    scan_status st = ssm_check("ssm_scan_step", batch, 1, d, n, groups, dtype, {u_stride, dt_stride, b_stride, c_stride, z_stride}, kMaxStride);
     if (st != SCAN_OK) return st;
     if (batch == 0) return SCAN_OK;
     const size_t es = dtype_size(dtype);

@@ -37,3 +37,22 @@ def test_a_last_launch_of_more_than_2_32_threads():
             assert (t == t[:1]).all(), m
             err, most = (t[:1].double() - ref[m]).abs(), tol[m]
         assert (err <= most).all(), (m, float(err.max()))
+
+
+@pytest.mark.parametrize("dtype", [bf, f32], ids=["bf16", "f32"])
+def test_single_tokens_of_long_rows(dtype):
+    """A token's slices of prompts whose rows lie 2^22 elements and more apart, as the same values one after the other."""
+    batch, length, width, n = 3, 2049, 2048, 4
+    say(f"[ssm] slices of long rows {dtype}")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    u = torch.randn(batch, length, width, generator=g, device="cuda").to(dtype)
+    both = torch.randn(batch, length, 2 * n + 2040, generator=g, device="cuda").to(dtype)
+    b, c = both[..., :n].unsqueeze(-2), both[..., n:2 * n].unsqueeze(-2)
+    a, h = -torch.rand(width, n, generator=g, device="cuda"), torch.randn(batch, width, n, generator=g, device="cuda")
+    for t in (0, 1000, length - 1):
+        one, two = h.clone(), h.clone()
+        assert u[:, t].stride(0) >= 1 << 22
+        y = ssm.ssm_scan_step(one, u[:, t], u[:, t], a, b[:, t], c[:, t], z=u[:, t])
+        x = u[:, t].contiguous()
+        want = ssm.ssm_scan_step(two, x, x, a, b[:, t].contiguous(), c[:, t].contiguous(), z=x)
+        assert torch.equal(y, want) and torch.equal(one, two) and not torch.equal(one, h)
