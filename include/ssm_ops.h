@@ -44,7 +44,8 @@ extern "C" {
  *   dtype, a row's groups * n values dense;  a f32 [d, n];  skip (d above) and
  *   dt_bias f32 [d], NULL = 0;  h0 f32 [batch, d, n], NULL = 0.
  * batch, length >= 0, 1 <= d <= 2^21 and a multiple of groups, 1 <= n <= SSM_MAX_STATE,
- * batch * length < 2^31, row strides below 2^22 (of a single token: up to 2^40).
+ * batch * length < 2^31, row strides below 2^22 (of a single token: up to 2^40), and fewer than
+ * 2^24 waves: batch * groups * ceil((d / groups) / (128 / g)), g = 2, 4, 8, 16 for n up to 8, 16, 32, 64.
  * ====================================================================== */
 #define SSM_MAX_STATE 64
 /* Tokens between two states that the forward keeps for the backward. */

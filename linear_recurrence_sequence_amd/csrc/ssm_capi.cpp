@@ -27,7 +27,8 @@ scan_status ssm_check(const char* fn, int64_t batch, int64_t length, int d, int 
         return fail(SCAN_ERR_SHAPE, std::string(fn) + ": unsupported shape batch=" + std::to_string(batch) + " length=" + std::to_string(length) +
                                         " d=" + std::to_string(d) + " n=" + std::to_string(n) + " groups=" + std::to_string(groups) +
                                         " (need d a multiple of groups, 1 <= n <= " + std::to_string(SSM_MAX_STATE) +
-                                        ", batch * length < 2^31 and launches below 2^32 threads)");
+                                        ", d <= 2^21, batch * length < 2^31 and fewer than 2^24 waves, one for each row and 128 / g channels of a group: g = 2, 4, 8, 16 for n up "
+                                        "to 8, 16, 32, 64)");
     if (!dtype_ok(dtype)) return fail(SCAN_ERR_SHAPE, std::string(fn) + ": dtype must be SCAN_BF16 or SCAN_F32");
     return check_strides(fn, strides, most_stride);
 }

@@ -79,14 +79,14 @@ inline SsmJoin ssm_join(int64_t batch, int64_t length, int d, int n, int groups,
     return j;
 }
 
-// Sizes that the launches cover: workgroups of 256 threads, and element counts within 62 bits.
+// Sizes that the launches cover: fewer than 2^24 waves forward and workgroups of 256 backward (the step has 16 threads a channel at most, which is
+// fewer; the last launch takes any number), and element counts within 62 bits.
 inline bool ssm_fits(int64_t batch, int64_t length, int d, int n, int groups) {
     if (!ssm_shape(batch, length, d, n, groups)) return false;
     const int64_t chunks = ceil_div(std::max<int64_t>(length, 1), SSM_TOK), most = MOST_THREADS / 256;
     const SsmPlan f = ssm_plan(batch, length, d, n, groups, false), b = ssm_plan(batch, length, d, n, groups, true);
     const __int128 state = (__int128)batch * chunks * d * SSM_MOST_N * 4, rows = (__int128)batch * length * groups;
     return (__int128)batch * groups * f.tiles * f.segments <= most && (__int128)batch * groups * b.blocks * b.segments <= most &&
-           (__int128)batch * d * 16 <= MOST_THREADS && rows * SSM_MOST_N * 2 <= MOST_THREADS && (__int128)d * SSM_MOST_N * 64 <= MOST_THREADS &&
            state < ((__int128)1 << 62) && rows * b.blocks * SSM_MOST_N * 8 < ((__int128)1 << 62);
 }
 

@@ -116,7 +116,7 @@ def _scan_args(u, dt, a, b, c, d, z, dt_bias, dims):
 
 def _workspace(need, workspace, device):
     if need == 0:
-        raise ValueError("unsupported shape: batch * length must stay below 2^31 and a launch below 2^32 threads")
+        raise ValueError("unsupported shape: batch * length must stay below 2^31, and launches below 2^32 threads (of the scan: 2^24 waves)")
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=device)
     _want_bytes(workspace, "workspace", need, device)

@@ -56,3 +56,40 @@ def test_single_tokens_of_long_rows(dtype):
         x = u[:, t].contiguous()
         want = ssm.ssm_scan_step(two, x, x, a, b[:, t].contiguous(), c[:, t].contiguous(), z=x)
         assert torch.equal(y, want) and torch.equal(one, two) and not torch.equal(one, h)
+
+
+@pytest.mark.parametrize("batch,length,d,n", [(32801, 1024, 1, 1), (1, 19, 1 << 21, 2)])
+def test_many_tokens_and_wide_rows(batch, length, d, n):
+    """More than 2^25 tokens, and the widest rows.  Every row holds the same tokens, and where it is wide the same channels over and over, so
+    that few of them in 64 bits say what all hold; db and dc add the channels up."""
+    say(f"[ssm] batch={batch} length={length} d={d} n={n}")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    few = min(d, 32)
+
+    def normal(*shape):
+        return torch.randn(shape, generator=g, device="cuda")
+
+    one = dict(u=normal(1, length, few), dt=normal(1, length, few), a=-torch.rand(few, n, generator=g, device="cuda") - 0.1,
+               b=normal(1, length, 1, n), c=normal(1, length, 1, n), d=normal(few), z=normal(1, length, few), dt_bias=normal(few) - 2)
+    dy = normal(1, length, few)
+    times = d // few
+    k = {m: t.repeat(batch, 1, times) if m in ("u", "dt", "z") else t.repeat(batch, 1, 1, 1) if m in ("b", "c") else t.repeat(times, *[1] * (t.dim() - 1))
+         for m, t in one.items()}
+    y, h, saved = ssm.ssm_scan_fwd(**k)
+    got = ssm.ssm_scan_bwd(*k.values(), saved, dy.repeat(batch, 1, times))
+    torch.cuda.synchronize()
+    got.update(y=y, h=h)
+    ref = scan_ref(**one, dy=dy)
+    tol = scan_tolerance(scan_ref(**one, dy=dy, absolute=True), ref, length, f32)
+    for m, t in got.items():
+        per, want, most = t, ref[m], tol[m]
+        if m in ("y", "du", "ddt", "dz"):
+            per = t.unflatten(2, (times, few))
+            want, most = want[:, :, None], most[:, :, None]
+        elif m == "h":
+            per, want, most = t.unflatten(1, (times, few)), want[:, None], most[:, None]
+        elif m in ("da", "dd", "ddt_bias"):                      # FP64 over the rows, rounded once more
+            per, want, most = t.unflatten(0, (times, few)), want[None] * batch, (most + U * want.abs())[None] * batch
+        else:                                                    # FP32 over 128 / g channels of a wave at a time, four waves, then workgroups one by one
+            want, most = want * times, (most + (times + 64) * U * tol[m] / (20 * (2 * length + 6) * U)) * times
+        assert ((per.double() - want).abs() <= most).all(), m

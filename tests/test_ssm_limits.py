@@ -26,3 +26,15 @@ def test_single_tokens_take_wide_row_strides():
     for name in ("us", "dts", "bs", "cs", "zs"):
         for stride, status in ((1 << 22, -6), (1 << 33, -6), ((1 << 40) + 1, -2), (-1, -2)):
             assert f(*{**step, name: stride, "h": P(4)}.values(), None) == status, (name, stride)
+
+
+def test_documented_sizes_are_accepted():
+    """batch * length below 2^31, d up to 2^21, and launches of fewer than 2^24 waves forward: nothing else bounds the sizes."""
+    from linear_recurrence_sequence_amd import ssm
+    size, saved = ssm.lib().ssm_scan_workspace_bytes, ssm.lib().ssm_scan_saved_bytes
+    for batch, length, d, n, groups, ok in ((1, 1 << 25, 1, 1, 1, True), (1, (1 << 31) - 257, 1, 64, 1, True), (1, 1 << 20, 64, 64, 64, True),
+                                            (1, 4, 1 << 21, 64, 1, True), (1, 4, (1 << 21) + 1, 1, 1, False), (64, 4, (1 << 21) - 8, 64, 1, True),
+                                            (65, 4, 1 << 21, 64, 1, False), ((1 << 24) - 1, 1, 1, 1, 1, True), (1 << 24, 1, 1, 1, 1, False),
+                                            (1 << 16, 1 << 15, 1, 1, 1, False)):
+        case = batch, length, d, n, groups
+        assert bool(size(*case, 0)) is ok and bool(size(*case, 1)) is ok and bool(saved(*case)) is ok, case
