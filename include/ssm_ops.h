@@ -18,8 +18,10 @@
  * there on are padding: their outputs and gradients are zero, what their
  * inputs hold is not used, and the state behind a row is the one after its
  * last token.  A length outside 0..length counts as the nearest of the two.
- * A flag in the padding starts an empty sequence for the scan, whose state behind
- * the row is then zero; the convolution looks at no flags there.
+ * The two operators differ on flags in the padding: for the scan one starts an empty
+ * sequence there, whose state behind the row is then zero; the convolution looks at no
+ * flags there and leaves the inputs of the row's last tokens.  Where single tokens go on
+ * from both states, clear the flags of padding first (reset and t < lengths).
  */
 #ifndef SSM_OPS_H
 #define SSM_OPS_H

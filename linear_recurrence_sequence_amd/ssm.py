@@ -15,7 +15,9 @@ Rows of activations may lie apart (views of a wider projection).  In all calls
 over several tokens, reset [batch, length] (uint8 or bool) marks tokens that
 start a sequence, and lengths [batch] (int32) says where a row's padding begins: its
 outputs and gradients are zero, and the state behind a row is the one after its
-last token (of the scan zero if a token of the padding is marked: an empty sequence starts there).
+last token.  Of the scan it is zero if a token of the padding is marked, an empty sequence
+starting there, while the convolution looks at no marks in the padding: where single tokens go
+on from both states, clear those marks first, reset & (arange(length) < lengths[:, None]).
 """
 import ctypes
 
