@@ -8,13 +8,20 @@
 //
 // Bound by the vector ALU, as the forward.  From the state that the forward kept before a chunk of 16 tokens the states of its later
 // half are formed again into registers (64: two channels by four states by eight tokens a lane) and walked from their end, then those
-// of its earlier half.  All 16 at once would spill 136 registers; a state kept every eight tokens would double what a user keeps.
+// of its earlier half.  All 16 at once, with 16 states, would spill 136 registers; a state kept every eight tokens would double what a user keeps.
+// Of more than 32 states all 16 tokens are held at once, since the sums over 16 lane groups take 16 tokens.
 // Sums over states (du, ddt, dz) are in the lane but for steps over the lane groups, which four tokens share;
 // sums over channels (db, dc) go through LDS: each token's eight values of a lane are summed eight lanes at a time, then over the
 // workgroup's waves, and the workgroups' parts are added by a last launch, in a fixed order.
 //
 // 32768 x 2048 channels x 16 states in BF16, gated and packed: the segments from zero 270 us, the backward 1100 to 1170 us, the last launch 19 us.
-// The vector ALU is busy for 77 and 70% of the first two's time; 256 registers and 75 KB of LDS a workgroup leave two waves a SIMD.
+// The vector ALU is busy for 77 and 70% of the first two's time.  What a gated wave holds, BF16 (FP32), and waves a SIMD:
+//   states      registers  spilled   LDS of a workgroup  waves
+//   up to 8     277 (308)  none      117 KB              one
+//   9 to 16     256 (256)  27 (78)   73 KB               two
+//   17 to 32    227 (234)  none      69 KB               two
+//   33 to 64    313 (317)  none      91 KB               one
+// 2 x 2048 x 2048 takes 170, 186, 295 and 802 us with 8, 16, 32 and 64 states (177, 208, 295 and 789), the launches before and after included.
 #include "ssm_lay.hpp"
 
 namespace lrs {
@@ -417,11 +424,10 @@ __device__ __forceinline__ void join_channel(const SsmArgs& a, int64_t x) {
     if (out) *out = (float)w;
 }
 template <class T>
-__global__ __launch_bounds__(256) void ssm_join_kernel(const SsmArgs a, const SsmJoin j) {
-    for (int64_t w = blockIdx.x; w < j.all; w += j.grid) {
-        if (w < j.narrow) join_narrow<T>(a, w * 256 + threadIdx.x);
-        else join_channel(a, (w - j.narrow) * 256 + threadIdx.x);
-    }
+__global__ __launch_bounds__(256) void ssm_join_kernel(const SsmArgs a, int64_t first, int64_t narrow) {
+    const int64_t w = first + blockIdx.x;
+    if (w < narrow) join_narrow<T>(a, w * 256 + threadIdx.x);
+    else join_channel(a, (w - narrow) * 256 + threadIdx.x);
 }
 
 template <class T, int NG, bool GATE>
@@ -449,7 +455,8 @@ void launch_bwd_any(const SsmArgs& a, hipStream_t s) {
         }
     }
     const SsmJoin j = ssm_join(a.batch, a.length, a.d, a.n, a.groups, a.plan.ng);
-    LRS_LAUNCH(K_SSM_JOIN, (ssm_join_kernel<T>), dim3(j.grid), dim3(256), 0, s, a, j);
+    for (int64_t w = 0; w < j.all; w += j.grid)
+        LRS_LAUNCH(K_SSM_JOIN, (ssm_join_kernel<T>), dim3((unsigned)std::min<int64_t>(j.grid, j.all - w)), dim3(256), 0, s, a, w, j.narrow);
 }
 
 }  // namespace

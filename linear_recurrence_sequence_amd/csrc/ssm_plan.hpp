@@ -41,8 +41,11 @@ struct SsmPlan {
 //   2 x 2048 x 2048          45 + 89    36 + 60    39 + 59    35 + 71    39 + 82
 //   1 x 32768 x 2048         330 + 644  260 + 383  249 + 362  241 + 372  240 + 368
 // More waves hide more, until each walks so few tokens that going through the segments before it (one state read for
-// each) costs more: three, which is what fits at once, where that leaves 256 tokens or more to each, else two.  The backward's
-// registers and LDS leave room for two: 2 x 2048 x 2048 with one, two and four 47 + 248, 40 + 173 and 39 + 187.
+// each) costs more: three where that leaves 256 tokens or more to each, else two.  In the backward two: 2 x 2048 x 2048 with one, two and four
+// 47 + 248, 40 + 173 and 39 + 187.  All of this was timed with 16 states.  Of these, three waves of the gated scan fit a SIMD at once and two
+// of the backward; up to 8 states two (FP32) or three and one, 17 to 32 two and two, 33 to 64 one and one.  The same plan serves them.
+// 64 segments are the most, so that a narrow row leaves SIMDs idle: 1 x 32768 takes 224 + 535 us at a width of 64, 243 + 541 at 512 and 529 + 1313
+// at 2048 (forward with the states kept, and backward).
 constexpr int64_t SIMDS = 1024;
 
 inline SsmPlan ssm_plan(int64_t batch, int64_t length, int d, int n, int groups, bool backward) {
@@ -66,7 +69,7 @@ inline bool ssm_shape(int64_t batch, int64_t length, int d, int n, int groups) {
 }
 
 // The backward's last launch: workgroups of 256 sums, first of db and dc (two values for each row, group and padded state), then of da, dskip and
-// ddt_bias (n + 2 for each channel).  Together they may need more threads than a launch has, so that a workgroup of the grid takes every grid-th.
+// ddt_bias (n + 2 for each channel).  Together they may need more threads than a launch has: then there are several, of `grid` workgroups at most.
 struct SsmJoin {
     int64_t narrow, all;  // workgroups of db and dc, and of everything
     unsigned grid;
