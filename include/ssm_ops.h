@@ -103,7 +103,8 @@ scan_status ssm_scan_step(int64_t batch, int d, int n, int groups, int dtype, in
  * sequence of the row count as zero.  Arithmetic is FP32, y is rounded once.
  *   x      [batch, length, d] of dtype;  w f32 [d, width];  bias f32 [d], NULL = 0
  *   state  [batch, width - 1, d] of dtype, dense, the oldest input first
- * batch, length >= 0, 1 <= d <= 2^24, batch * length < 2^31.
+ * batch, length >= 0, 1 <= d <= 2^24, batch * length < 2^31, and launches below 2^32
+ * threads: batch * pieces * ceil(d / 2) of pieces of 8 to 64 tokens.
  * ====================================================================== */
 enum { CONV_NONE = 0, CONV_SILU = 1 };
 #define CONV_MAX_WIDTH 4

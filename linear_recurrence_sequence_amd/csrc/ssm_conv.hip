@@ -10,7 +10,8 @@
 // the other as they are complete.  A sequence's start clears what is held.
 //
 // 32768 x 2560 in BF16 with SiLU, packed: forward 64 us, 5.3 TB/s; backward 126 us, 4.0 TB/s, and 13 us for the sums (a copy of the same input takes 60 us, a sum of
-// two tensors 86).  Four channels a lane forward, two backward, whose sums and cotangents would else take 200 registers (235 us).
+// two tensors 86).  In FP32 129 us, and 349 with the sums, with three taps 213: the four-tap backward spills 9 to 12 of its 128 registers there.
+// Four channels a lane forward, two backward, whose sums and cotangents would else take 200 registers (235 us).
 #include "lm.hpp"
 #include "ssm_lay.hpp"
 

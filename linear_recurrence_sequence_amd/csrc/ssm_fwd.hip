@@ -13,6 +13,8 @@
 //
 // 32768 x 2048 channels x 16 states in BF16, gated and packed: the segments from zero 240 us, the scan with the states kept for
 // the backward 350 us, 3.0 T state updates a second; the vector ALU is busy for 81 and 79% of the time.
+// Registers of the gated scan, and waves a SIMD (BF16; FP32): up to 8 states 154, three (169, two); 9 to 16 138, three (150, three);
+// 17 to 32 181, two (187, two); 33 to 64 288, one (291, one), as a token's sums over 16 lane groups are formed for 16 tokens at once.  Nothing spills.
 #include "ssm_lay.hpp"
 
 namespace lrs {
