@@ -23,7 +23,8 @@ struct SsmArgs {
     const int32_t* lengths;
     void* y;
     float *h, *saved;                      // h: final states; saved [batch, chunks, n, d]: the states before each chunk
-    float* part;                           // [batch, segments, 2, n, d]: root of the product of a segment's decays (SEGMENT_STARTS: a sequence starts in it), state (cotangent) leaving it from zero
+    float* part;                           // [batch, segments, 2, n, d]: root of the product of a segment's decays (SEGMENT_STARTS: a sequence
+                                           // starts in it), state (cotangent) leaving it from zero
     // backward
     const void* dy;
     int64_t dy_stride;

@@ -42,3 +42,19 @@ def test_the_largest_vocabulary():
     assert sum(int(p.count_nonzero()) for p in dw.split(1 << 28)) == 4
     out = lm.embed_fwd(t, dw)
     assert torch.equal(out[[0, 1, 2, 3, 4, 6], 0].float().cpu(), torch.tensor([5.0, 2.0, 5.0, 8.0, 0.0, 64.0])) and out[5].isnan().all()
+
+
+def test_the_most_tokens():
+    """Seven rows of about 9.6 million tokens each: counts below 2^24, which FP32 adds up exactly in any order."""
+    n, v = (1 << 26) - 64, 7
+    say(f"[embed] n={n} v={v}")
+    t = torch.randint(0, v, (n,), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    t[::1000] = -1
+    counts = torch.bincount(t[t >= 0], minlength=v)
+    assert int(counts.max()) < 1 << 24
+    dout = torch.ones(1, 3, device="cuda").expand(n, 3)
+    assert torch.equal(lm.embed_bwd(t, dout, v, grad_dtype=f32).double(), counts.double()[:, None].expand(v, 3))
+    w = torch.arange(21, device="cuda", dtype=f32).view(v, 3) + 1
+    out = lm.embed_fwd(t, w, out_dtype=bf)
+    assert torch.equal(out[-70000:], torch.where((t[-70000:] >= 0)[:, None], w[t[-70000:].clamp_min(0)], 0).to(bf))
+    assert torch.equal(out[:, 0].float(), torch.where(t >= 0, 3.0 * t + 1, 0.0))
